@@ -3,6 +3,7 @@ import ctypes
 
 c_int, c_int32, c_int64, c_float, c_void_p, c_char_p = (ctypes.c_int, ctypes.c_int32, ctypes.c_int64, ctypes.c_float,
                                                        ctypes.c_void_p, ctypes.c_char_p)
+c_double = ctypes.c_double
 P = ctypes.POINTER
 
 
@@ -27,6 +28,12 @@ class pcd_stats(ctypes.Structure):
     _fields_ = [("prefill_ms", c_float), ("compile_ms", c_float), ("branch_ms", c_float), ("readout_ms", c_float),
                 ("total_ms", c_float), ("forward_passes", c_int), ("branch_tokens", c_int), ("readout_rows", c_int),
                 ("h2d_bytes", c_int64), ("d2h_bytes", c_int64)]
+
+
+class pcd_kv_pages(ctypes.Structure):
+    _fields_ = [("k", c_void_p), ("v", c_void_p), ("k_scale", c_void_p), ("v_scale", c_void_p),
+                ("page_stride", c_int64), ("head_stride", c_int64), ("token_stride", c_int64), ("n_pages", c_int),
+                ("page_size", c_int), ("n_kv_heads", c_int), ("head_dim", c_int), ("format", c_int)]
 
 
 # (name, restype, argtypes) of every entry point declared in include/*.h
@@ -74,6 +81,16 @@ SIGNATURES = [
     ("pcd_k_wait_probe", c_int, [c_int64, c_void_p, c_void_p, c_void_p]),
     ("pcd_k_gemm_swap", c_int, [c_void_p, c_void_p, c_int, c_int, c_void_p, c_int, c_int, c_int, c_int, c_void_p,
                                 c_int, c_int, c_void_p, c_void_p]),
+    ("pcd_rope_freqs", c_int, [c_int, c_double, c_int, c_double, c_double, c_double, c_double, c_void_p, P(c_float)]),
+    ("pcd_k_rope", c_int, [c_void_p, c_void_p, c_int, c_int, c_int, c_int, c_int64, c_int64, c_int64, c_int64, c_void_p,
+                           c_int, c_int, c_float, c_void_p, c_int, c_int, c_void_p]),
+    ("pcd_k_kv_append", c_int, [P(pcd_kv_pages), c_void_p, c_void_p, c_int, c_int64, c_int64, c_int64, c_int64,
+                                c_void_p, c_void_p, c_void_p, c_int, c_int, c_int, c_void_p, c_int, c_int, c_float,
+                                c_void_p, c_void_p, c_void_p]),
+    ("pcd_k_paged_attention_scratch_bytes", c_int64, [c_int, c_int, c_int, c_int, c_int, c_int64]),
+    ("pcd_k_paged_attention", c_int, [P(pcd_kv_pages), c_void_p, c_void_p, c_void_p, c_int, c_int, c_int64, c_int64,
+                                      c_int64, c_int64, c_void_p, c_void_p, c_void_p, c_int, c_int, c_int, c_int64,
+                                      c_int, c_float, c_void_p, c_int64, c_void_p, c_void_p]),
 ]
 
 

@@ -33,6 +33,10 @@ int fail(int code, const std::string& msg) {
 }
 }  // namespace
 
+namespace pcd {
+int set_error(int code, const char* detail) { return fail(code, detail); }
+}  // namespace pcd
+
 #define PCD_CUDA(x)                                                                                   \
   do {                                                                                                \
     cudaError_t e_ = (x);                                                                             \

@@ -1,0 +1,554 @@
+// Rotary positions, the append to an 8-bit paged K/V cache and the attention
+// over it for few query rows.
+#include <algorithm>
+#include <cstdint>
+
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+
+#include "common.cuh"
+#include "paged.cuh"
+#include "paged.h"
+#include "pcd.h"
+#include "pcd_kernels.h"
+#include "warp_mma.cuh"
+
+namespace pcd {
+namespace {
+
+// ======================================================================== rope
+// y = R x per pair; the angle is p F mod 1 turn in 64-bit integers, so it is
+// as exact at position 2^31 as at 1.  One thread a pair.
+template <class T>
+__global__ void rope_kernel(RopeKArgs a) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int half = a.rope.rot / 2, rest = a.dim - a.rope.rot;
+  const int units = half + rest;
+  const int64_t idx = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
+  const int64_t total = static_cast<int64_t>(a.n_tok) * a.heads * units;
+  if (idx >= total) return;
+  const int u = static_cast<int>(idx % units);
+  const int64_t th = idx / units;
+  const int h = static_cast<int>(th % a.heads);
+  const int64_t t = th / a.heads;
+  const T* x = static_cast<const T*>(a.x) + t * a.x_tok + h * a.x_head;
+  T* y = static_cast<T*>(a.y) + t * a.y_tok + h * a.y_head;
+  if (u >= half) {
+    y[a.rope.rot + u - half] = x[a.rope.rot + u - half];
+    return;
+  }
+  float c, s;
+  turn(a.pos ? a.pos[t] : a.base + static_cast<int>(t), a.rope.freqs[u], &c, &s);
+  c *= a.rope.amp;
+  s *= a.rope.transpose ? -a.rope.amp : a.rope.amp;
+  const int i = a.rope.interleaved ? 2 * u : u, j = a.rope.interleaved ? 2 * u + 1 : u + half;
+  const float p = to_f(x[i]), q = to_f(x[j]);
+  y[i] = from_f<T>(p * c - q * s);
+  y[j] = from_f<T>(q * c + p * s);
+}
+
+}  // namespace
+
+int launch_rope(const RopeKArgs& a, cudaStream_t s) {
+  if (a.n_tok == 0 || a.heads == 0) return 0;
+  const int64_t total = static_cast<int64_t>(a.n_tok) * a.heads * (a.dim - a.rope.rot / 2);
+  const dim3 grid(static_cast<unsigned>((total + 255) / 256));
+  switch (a.dtype) {
+    case PCD_DTYPE_F32: return launch_k(rope_kernel<float>, grid, dim3(256), 0, s, a);
+    case PCD_DTYPE_BF16: return launch_k(rope_kernel<__nv_bfloat16>, grid, dim3(256), 0, s, a);
+    default: return launch_k(rope_kernel<__half>, grid, dim3(256), 0, s, a);
+  }
+}
+
+namespace {
+// ====================================================================== append
+// One CTA owns one (page, KV head) of K or of V that a sequence's new tokens
+// touch: nothing else writes it, so the block's scale needs no atomics and
+// comes out the same on every run.
+//   amax over the new rows -> scale (grown, never shrunk, while older tokens
+//   stay in the page) -> older codes rescaled if it grew -> new codes.
+constexpr int kAppendThreads = 128;
+
+template <class T>
+__device__ __forceinline__ float append_value(const AppendArgs& a, bool is_v, const T* row, int d, int pos) {
+  if (is_v || d >= a.rope.rot) return to_f(row[d]);
+  const int half = a.rope.rot / 2;
+  int i, j, u;
+  bool second;
+  if (a.rope.interleaved) {
+    u = d >> 1;
+    i = d & ~1;
+    j = i + 1;
+    second = d & 1;
+  } else {
+    second = d >= half;
+    u = second ? d - half : d;
+    i = u;
+    j = u + half;
+  }
+  float c, s;
+  turn(pos, a.rope.freqs[u], &c, &s);
+  c *= a.rope.amp;
+  s *= a.rope.amp;
+  const float p = to_f(row[i]), q = to_f(row[j]);
+  return second ? q * c + p * s : p * c - q * s;
+}
+
+template <class T>
+__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(AppendArgs a) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const int page = 1 << a.c.page_log2;
+  const int h = blockIdx.y;
+  const bool is_v = blockIdx.z != 0;
+  const int tid = threadIdx.x, lane = tid & 31;
+  // item -> (sequence, page of its new range)
+  const SeqItem it = find_item(a.q, static_cast<int>(blockIdx.x), 1, a.c.page_log2, 2);
+  if (it.seq < 0) return;
+  const int n = it.n, len = a.q.kv_len[it.seq];
+  if (n == 0) return;
+  if (n < 0 || it.row0 < 0 || n > a.q.n_tok - it.row0 || len < n || len > kMaxLen ||
+      len > static_cast<int64_t>(a.q.table_stride) << a.c.page_log2) {
+    if (tid == 0) record_error(a.err, DEV_BAD_INDEX);
+    return;
+  }
+  if (it.local > (n >> a.c.page_log2) + 1) return;
+  const int start = len - n;
+  const int pg = (start >> a.c.page_log2) + it.local;
+  const int lo = max(pg << a.c.page_log2, start), hi = min((pg + 1) << a.c.page_log2, len);
+  if (lo >= hi) return;
+  const int id = a.q.table[static_cast<int64_t>(it.seq) * a.q.table_stride + pg];
+  if (id < 0 || id >= a.c.n_pages) {
+    if (tid == 0) record_error(a.err, DEV_BAD_INDEX);
+    return;
+  }
+  const int held = lo & (page - 1), rows = hi - lo, D = a.c.dim;
+  const int t0 = it.row0 + (lo - start);
+  const T* src = static_cast<const T*>(is_v ? a.v : a.k) + (is_v ? a.v_head : a.k_head) * h;
+  const int64_t ts = is_v ? a.v_tok : a.k_tok;
+  uint8_t* dst = (is_v ? a.c.v : a.c.k) + id * a.c.page_stride + h * a.c.head_stride;
+  float* sc = (is_v ? a.c.vs : a.c.ks) + static_cast<int64_t>(id) * a.c.Hkv + h;
+
+  // |x| as integers: their order is the floats', and a NaN beats everything
+  uint32_t am = 0;
+  for (int e = tid; e < rows * D; e += kAppendThreads) {
+    const int r = e / D, d = e - r * D;
+    const int p = a.pos ? a.pos[t0 + r] : lo + r;
+    am = max(am, __float_as_uint(append_value(a, is_v, src + (t0 + r) * ts, d, p)) & 0x7fffffffu);
+  }
+  __shared__ uint32_t red[kAppendThreads / 32];
+  am = __reduce_max_sync(0xffffffffu, am);
+  if (lane == 0) red[tid >> 5] = am;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kAppendThreads / 32; ++w) am = max(am, red[w]);
+  const float old = held ? *sc : 0.f;
+  const float scale = block_scale(__uint_as_float(am), old, held > 0, a.c.format);
+  __syncthreads();  // every thread has read the old scale
+  if (tid == 0) *sc = scale;
+  if (held && !(scale == old)) {
+    const float ratio = old / scale;
+    for (int e = tid; e < held * D; e += kAppendThreads) {
+      const int r = e / D, d = e - r * D;
+      uint8_t* q = dst + r * a.c.tok_stride + d;
+      *q = encode(decode(*q, a.c.format) * ratio, a.c.format);
+    }
+  }
+  const float inv = 1.f / scale;
+  for (int e = tid; e < rows * D; e += kAppendThreads) {
+    const int r = e / D, d = e - r * D;
+    const int p = a.pos ? a.pos[t0 + r] : lo + r;
+    dst[(held + r) * a.c.tok_stride + d] =
+        encode(append_value(a, is_v, src + (t0 + r) * ts, d, p) * inv, a.c.format);
+  }
+}
+
+}  // namespace
+
+int launch_kv_append(const AppendArgs& a, cudaStream_t s) {
+  if (a.q.n_tok == 0 || a.q.n_seq == 0) return 0;
+  const int64_t items = (static_cast<int64_t>(a.q.n_tok) >> a.c.page_log2) + 2ll * a.q.n_seq;
+  const dim3 grid(static_cast<unsigned>(items), static_cast<unsigned>(a.c.Hkv), 2);
+  switch (a.dtype) {
+    case PCD_DTYPE_F32: return launch_k(kv_append_kernel<float>, grid, dim3(kAppendThreads), 0, s, a);
+    case PCD_DTYPE_BF16: return launch_k(kv_append_kernel<__nv_bfloat16>, grid, dim3(kAppendThreads), 0, s, a);
+    default: return launch_k(kv_append_kernel<__half>, grid, dim3(kAppendThreads), 0, s, a);
+  }
+}
+
+namespace {
+// =================================================================== attention
+// Few query rows (16 to a tile: tokens x the G query heads of one KV head),
+// warp tensor-core MMA.
+//
+// Every warp walks its own 16-key blocks of the tile's key range with a
+// private cp.async ring, so no barrier stands in the key loop.  Codes become
+// fp16 in registers, exactly.  With S = q . k8 and block scales sk, sv,
+//   x = S sk c + log2 sv       (c = softmax scale x log2 e)
+//   w = exp2(x - M + 8)        M: a running reference no lower than max x - 7
+//   O += w v8,  l += w / sv,   out = O / l
+// so the value's scale rides in the exponent: w <= 2^15 fits fp16 whatever the
+// scales, and no value is rounded before the product.  Weights 2^-33 of the
+// largest are the first that fp16 loses; l keeps them in fp32.
+//
+// The channel order inside a dot product is free, so the K fragments are taken
+// as each lane's 16 consecutive bytes (Q's fragments are loaded in the same
+// order), and a V fragment's column is any channel, so a lane reads 16
+// consecutive channels of its four keys and pairs keys by byte permutes: no
+// ldmatrix, no transposition in shared memory.
+constexpr float kSlack = 7.f;
+constexpr int kWarps = 4, kStagesR = 4;
+
+template <int D>
+struct RowsCfg {
+  static constexpr int kStage = 16 * D * 2;                       // 16 keys: K then V
+  static constexpr int kRing = kWarps * kStagesR * kStage;
+  static constexpr int kRedLd = D + 4;
+  static constexpr int kRed = kWarps * 16 * (kRedLd * 4 + 8);     // partial rows after the key loop
+  static constexpr int kSmem = kRing > kRed ? kRing : kRed;
+};
+
+template <int D, int FMT, class T>
+__global__ void __launch_bounds__(kWarps * 32, 3) paged_attn_rows_kernel(PagedAttnArgs a) {
+  using C = RowsCfg<D>;
+  extern __shared__ __align__(16) uint8_t smem[];
+  griddep_launch_dependents();
+  griddep_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, c = lane & 3;
+  const int hk = blockIdx.y, z = blockIdx.z;
+  const SeqItem it = find_item(a.q, static_cast<int>(blockIdx.x), a.G, 4, 1);
+  if (it.seq < 0) return;
+  const int n = it.n;
+  if (n == 0) return;
+  if (n < 0 || it.row0 < 0 || n > a.q.n_tok - it.row0) {
+    if (threadIdx.x == 0) record_error(a.err, DEV_BAD_INDEX);
+    return;
+  }
+  int len = a.q.kv_len[it.seq];
+  if (len < 0 || len > kMaxLen || len > static_cast<int64_t>(a.q.table_stride) << a.c.page_log2) {
+    if (threadIdx.x == 0) record_error(a.err, DEV_BAD_INDEX);
+    len = 0;
+  }
+  const int R = n * a.G;
+  if (it.local >= (R + 15) >> 4) return;
+  const int r0 = it.local * 16;
+  const int r_end = min(r0 + 16, R);
+  // keys seen by a row: all, or up to its own position
+  const int first = a.causal ? len - n + 1 : len;  // by the sequence's first token
+  auto seen = [&](int r) { return a.causal ? first + min(r, R - 1) / a.G : len; };
+  const int kmax = max(0, seen(r_end - 1));
+  const int kmin = max(0, seen(r0));
+  const int b0 = z * (a.split_len >> 4);
+  const int b1 = z + 1 < a.n_splits ? min((kmax + 15) >> 4, b0 + (a.split_len >> 4)) : (kmax + 15) >> 4;
+  const int nb = b1 > b0 + warp ? (b1 - b0 - warp + kWarps - 1) / kWarps : 0;  // blocks of this warp
+
+  // ---- Q fragments: k-step t takes channels (64 * (t / 4) + 16 c + 4 (t % 4)) + {0, 1 | 2, 3}
+  uint32_t qf[D / 16][4];
+  float qs[2];
+  float row_m[2] = {-INFINITY, -INFINITY}, row_l[2] = {0.f, 0.f};
+  int vis[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int r = r0 + g + 8 * e;
+    vis[e] = seen(r);
+    const bool ok = r < R;
+    const int tok = it.row0 + (ok ? r : r0) / a.G, hq = hk * a.G + (ok ? r : r0) % a.G;
+    const T* src = static_cast<const T*>(a.x) + tok * a.x_tok + hq * a.x_head;
+    float v[D / 16][4];
+    uint32_t am = 0;
+#pragma unroll
+    for (int t = 0; t < D / 16; ++t) {
+      const int d = 64 * (t >> 2) + 16 * c + 4 * (t & 3);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        v[t][i] = ok ? to_f(src[d + i]) : 0.f;
+        am = max(am, __float_as_uint(v[t][i]) & 0x7fffffffu);
+      }
+    }
+    am = max(am, __shfl_xor_sync(0xffffffffu, am, 1));
+    am = max(am, __shfl_xor_sync(0xffffffffu, am, 2));
+    float down;
+    qs[e] = row_power<T>(am, &down);
+#pragma unroll
+    for (int t = 0; t < D / 16; ++t) {
+      qf[t][e] = pack2(v[t][0] * down, v[t][1] * down);
+      qf[t][2 + e] = pack2(v[t][2] * down, v[t][3] * down);
+    }
+    qs[e] *= a.scale_log2 * (FMT == PCD_KV_E4M3 ? 256.f : 1.f);  // fp8_half: codes read as 2^-8 of themselves
+  }
+
+  float o[D / 8][4];
+#pragma unroll
+  for (int t = 0; t < D / 8; ++t)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[t][i] = 0.f;
+
+  uint8_t* ring = smem + warp * (kStagesR * C::kStage);
+  const int32_t* tab = a.q.table + static_cast<int64_t>(it.seq) * a.q.table_stride;
+  const uint8_t* kbase = a.c.k + hk * a.c.head_stride;
+  const uint8_t* vbase = a.c.v + hk * a.c.head_stride;
+  // page ids of 32 of this warp's blocks at a time, one to a lane
+  int ids = -1;
+  float sk = 0.f, sv = 0.f;
+  int ids_base = -32;
+  int nids = -1;  // the next 32
+  auto block_at = [&](int i) { return b0 + warp + i * kWarps; };
+  auto fetch_ids = [&](int i0) {
+    const int i = i0 + lane;
+    int id = -1;
+    if (i < nb) {
+      id = tab[block_at(i) >> (a.c.page_log2 - 4)];
+      if (id < 0 || id >= a.c.n_pages) {
+        record_error(a.err, DEV_BAD_INDEX);
+        id = -1;
+      }
+    }
+    return id;
+  };
+  nids = fetch_ids(0);
+  auto issue = [&](int i) {
+    if (i < nb) {
+      if (i - ids_base >= 32) {  // the loads run ahead of the arithmetic by less than 32 blocks
+        ids = nids;
+        ids_base = i;
+        nids = fetch_ids(i + 32);
+      }
+      const int id = __shfl_sync(0xffffffffu, ids, i - ids_base);
+      const int slot = (block_at(i) << 4) & ((1 << a.c.page_log2) - 1);
+      uint8_t* st = ring + (i % kStagesR) * C::kStage;
+      const int64_t off = (id < 0 ? 0 : id) * a.c.page_stride + slot * a.c.tok_stride;
+      constexpr int kCh = D / 16;
+#pragma unroll
+      for (int e = 0; e < kCh / 2; ++e) {
+        const int x = e * 32 + lane, key = x / kCh, ch = x % kCh;
+        cp_async16(st + key * D + ((ch ^ ((key & 1) << 2)) & (kCh - 1)) * 16, kbase + off + key * a.c.tok_stride + ch * 16, id >= 0);
+        cp_async16(st + 16 * D + key * D + ((ch ^ (((key >> 1) & 3) << 1)) & (kCh - 1)) * 16, vbase + off + key * a.c.tok_stride + ch * 16, id >= 0);
+      }
+    }
+    cp_async_commit();
+  };
+  // scales of 32 blocks at a time
+  int cur_base = -32;
+  auto scales = [&](int i) {
+    if (i - cur_base >= 32) {
+      cur_base = i;
+      const int id = fetch_ids(i);
+      sk = id >= 0 ? a.c.ks[static_cast<int64_t>(id) * a.c.Hkv + hk] : 0.f;
+      sv = id >= 0 ? a.c.vs[static_cast<int64_t>(id) * a.c.Hkv + hk] : -1.f;
+      if (id >= 0 && sv < kScaleFloor) sv = kScaleFloor;  // a NaN stays
+    }
+  };
+
+#pragma unroll 1
+  for (int i = 0; i < kStagesR - 1; ++i) issue(i);
+#pragma unroll 1
+  for (int i = 0; i < nb; ++i) {
+    cp_async_wait<kStagesR - 2>();
+    __syncwarp();
+    issue(i + kStagesR - 1);
+    scales(i);
+    const float bsk = __shfl_sync(0xffffffffu, sk, i - cur_base);
+    const float bsv = __shfl_sync(0xffffffffu, sv, i - cur_base);
+    const uint8_t* st = ring + (i % kStagesR) * C::kStage;
+    // ---- S = Q K^T: two tiles of 8 keys
+    float s[2][4];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
+      const int key = 8 * t + g;
+#pragma unroll
+      for (int hf = 0; hf < D / 64; ++hf) {
+        const int ch = c + 4 * hf;
+        const uint4 w = *reinterpret_cast<const uint4*>(st + key * D + ((ch ^ ((key & 1) << 2)) & (D / 16 - 1)) * 16);
+        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          uint32_t h0, h1;
+          codes4_half<FMT>(ww[q], &h0, &h1);
+          mma16816(s[t], qf[4 * hf + q], h0, h1);
+        }
+      }
+    }
+    // ---- weights
+    const int j0 = block_at(i) << 4;
+    const float lsv = lg2(bsv);
+    const float isv = 1.f / bsv;
+    const bool bad = bsv == -1.f;  // a page the table has wrong: nothing of it is seen
+    float ak[2];
+    ak[0] = qs[0] * bsk;
+    ak[1] = qs[1] * bsk;
+    if (j0 + 16 > kmin || bad) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int j = j0 + 8 * t + 2 * c + (e & 1);
+          const float x = fmaf(s[t][e], ak[e >> 1], lsv);
+          s[t][e] = (j < vis[e >> 1] && !bad) ? x : -INFINITY;
+        }
+    } else {
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[t][e] = fmaf(s[t][e], ak[e >> 1], lsv);
+    }
+    float mx[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      mx[e] = fmaxf(fmaxf(s[0][2 * e], s[0][2 * e + 1]), fmaxf(s[1][2 * e], s[1][2 * e + 1]));
+    if (__any_sync(0xffffffffu, mx[0] > row_m[0] + kSlack || mx[1] > row_m[1] + kSlack)) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float m = mx[e];
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+        m = fmaxf(m, row_m[e]);
+        const float f = row_m[e] == -INFINITY ? 0.f : ex2_approx(row_m[e] - m);
+        row_m[e] = m;
+        row_l[e] *= f;
+#pragma unroll
+        for (int t = 0; t < D / 8; ++t) {
+          o[t][2 * e] *= f;
+          o[t][2 * e + 1] *= f;
+        }
+      }
+    }
+    float mb[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) mb[e] = (row_m[e] == -INFINITY ? 0.f : row_m[e]) - kBias;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        s[t][e] = ex2_approx(s[t][e] - mb[e >> 1]);
+        row_l[e >> 1] = fmaf(s[t][e], bad ? 0.f : isv, row_l[e >> 1]);
+      }
+    const uint32_t pf[4] = {pack2(s[0][0], s[0][1]), pack2(s[0][2], s[0][3]), pack2(s[1][0], s[1][1]),
+                            pack2(s[1][2], s[1][3])};
+    // ---- O += P V: column tile t's lane group g is channel g * (D / 8) + t
+    const uint8_t* sv_ = st + 16 * D;
+    constexpr int kLd = D / 8;  // channels of a lane: 16 or 8 bytes
+    uint32_t vr[4][kLd / 4];
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk) {
+      const int key = 2 * c + (kk & 1) + 8 * (kk >> 1);
+      const int byte = g * kLd, ch = byte >> 4;
+      const uint8_t* p = sv_ + key * D + ((ch ^ (((key >> 1) & 3) << 1)) & (D / 16 - 1)) * 16 + (byte & 15);
+      if constexpr (kLd == 16) {
+        const uint4 w = *reinterpret_cast<const uint4*>(p);
+        vr[kk][0] = w.x, vr[kk][1] = w.y, vr[kk][2] = w.z, vr[kk][3] = w.w;
+      } else {
+        const uint2 w = *reinterpret_cast<const uint2*>(p);
+        vr[kk][0] = w.x, vr[kk][1] = w.y;
+      }
+    }
+#pragma unroll
+    for (int t = 0; t < D / 8; ++t) {
+      const uint32_t v0 = codes_pair_half<FMT>(vr[0][t >> 2], vr[1][t >> 2], t & 3);
+      const uint32_t v1 = codes_pair_half<FMT>(vr[2][t >> 2], vr[3][t >> 2], t & 3);
+      mma16816(o[t], pf, v0, v1);
+    }
+    __syncwarp();
+  }
+  cp_async_wait<0>();
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    row_l[e] += __shfl_xor_sync(0xffffffffu, row_l[e], 1);
+    row_l[e] += __shfl_xor_sync(0xffffffffu, row_l[e], 2);
+  }
+  // ---- join the warps
+  __syncthreads();
+  float* red = reinterpret_cast<float*>(smem);
+  float2* ml = reinterpret_cast<float2*>(smem + kWarps * 16 * C::kRedLd * 4);
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int r = g + 8 * e;
+    if (c == 0) ml[warp * 16 + r] = make_float2(row_m[e], row_l[e]);
+#pragma unroll
+    for (int t = 0; t < D / 8; ++t)  // accumulator column 2c + i is lane group 2c + i's channel
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        red[(warp * 16 + r) * C::kRedLd + (2 * c + i) * (D / 8) + t] = o[t][2 * e + i];
+  }
+  __syncthreads();
+  for (int x = threadIdx.x; x < (r_end - r0) * (D / 4); x += kWarps * 32) {
+    const int r = x / (D / 4), d = (x % (D / 4)) * 4;
+    RowState st;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) st.top(ml[w * 16 + r]);
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w)
+      st.add(ml[w * 16 + r], *reinterpret_cast<const float4*>(red + (w * 16 + r) * C::kRedLd + d));
+    const int rr = r0 + r, tok = it.row0 + rr / a.G, hq = hk * a.G + rr % a.G;
+    finish_row<T>(a, st, z, tok, hq, d, FMT == PCD_KV_E4M3 ? 256.f : 1.f);
+  }
+}
+
+// Joins the key ranges of a row: out = sum 2^(M_i - M) O_i / sum 2^(M_i - M) l_i.
+template <int D, class T>
+__global__ void __launch_bounds__(256) paged_attn_join_kernel(PagedAttnArgs a, float unit) {
+  griddep_launch_dependents();
+  griddep_wait();
+  constexpr int kPer = D / 4;  // threads of a row
+  const int64_t row = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) / kPer;
+  const int d = (threadIdx.x % kPer) * 4;
+  const int64_t rows = static_cast<int64_t>(a.q.n_tok) * a.Hq;
+  if (row >= rows) return;
+  const int tok = static_cast<int>(row / a.Hq), hq = static_cast<int>(row % a.Hq);
+  if (tok < a.q.q_off[0] || tok >= a.q.q_off[a.q.n_seq]) return;  // rows of no sequence stay as they are
+  RowState st;
+  for (int z = 0; z < a.n_splits; ++z) st.top(a.part_ml[z * rows + row]);
+  for (int z = 0; z < a.n_splits; ++z) {
+    const float2 ml = a.part_ml[z * rows + row];
+    if (ml.y == 0.f) continue;
+    st.add(ml, *reinterpret_cast<const float4*>(a.part_o + (z * rows + row) * D + d));
+  }
+  PagedAttnArgs b = a;
+  b.n_splits = 1;
+  finish_row<T>(b, st, 0, tok, hq, d, unit);
+}
+
+template <int D, int FMT, class T>
+int launch_rows(const PagedAttnArgs& a, cudaStream_t s) {
+  using C = RowsCfg<D>;
+  auto kern = paged_attn_rows_kernel<D, FMT, T>;
+  cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  if (r != cudaSuccess) return r;
+  const int64_t items = ((static_cast<int64_t>(a.q.n_tok) * a.G) >> 4) + a.q.n_seq;
+  r = launch_k(kern, dim3(static_cast<unsigned>(items), static_cast<unsigned>(a.c.Hkv), static_cast<unsigned>(a.n_splits)),
+               dim3(kWarps * 32), C::kSmem, s, a);
+  if (r != cudaSuccess || a.n_splits == 1) return r;
+  const int64_t rows = static_cast<int64_t>(a.q.n_tok) * a.Hq;
+  return launch_k(paged_attn_join_kernel<D, T>, dim3(static_cast<unsigned>((rows * (D / 4) + 255) / 256)), dim3(256), 0, s, a,
+                  FMT == PCD_KV_E4M3 ? 256.f : 1.f);
+}
+
+template <int D, int FMT>
+int launch_rows_t(const PagedAttnArgs& a, cudaStream_t s) {
+  return a.dtype == PCD_DTYPE_BF16 ? launch_rows<D, FMT, __nv_bfloat16>(a, s) : launch_rows<D, FMT, __half>(a, s);
+}
+
+}  // namespace
+
+void plan_paged_attention(int n_tok, int n_seq, int G, int Hkv, int dim, int64_t max_kv, int sms, int* n_splits,
+                          int* split_len) {
+  const int64_t per = n_seq > 0 ? (n_tok + n_seq - 1) / n_seq : 0;
+  const int64_t tiles = std::max<int64_t>(1, n_seq * ((per * G + 15) / 16) * Hkv);
+  int64_t want = std::max<int64_t>(1, (static_cast<int64_t>(sms) * 12 + tiles - 1) / tiles);
+  want = std::min<int64_t>(want, 256);
+  int64_t len = (max_kv + want - 1) / want;
+  len = std::max<int64_t>(64, (len + 63) / 64 * 64);
+  *split_len = static_cast<int>(std::min<int64_t>(len, 1 << 30));
+  *n_splits = static_cast<int>(std::max<int64_t>(1, (max_kv + len - 1) / len));
+}
+
+int launch_paged_attention(const PagedAttnArgs& a, cudaStream_t s) {
+  if (a.q.n_tok == 0 || a.q.n_seq == 0) return 0;
+  const bool f8 = a.c.format == PCD_KV_E4M3;
+  if (a.c.dim == 64) return f8 ? launch_rows_t<64, PCD_KV_E4M3>(a, s) : launch_rows_t<64, PCD_KV_INT8>(a, s);
+  return f8 ? launch_rows_t<128, PCD_KV_E4M3>(a, s) : launch_rows_t<128, PCD_KV_INT8>(a, s);
+}
+
+}  // namespace pcd

@@ -1,0 +1,188 @@
+// Device helpers of the 8-bit paged K/V cache and of rotary positions.
+#pragma once
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cstdint>
+#include <type_traits>
+
+#include "common.cuh"
+#include "paged.h"
+#include "pcd_kernels.h"
+#include "ptx.cuh"
+
+namespace pcd {
+
+__device__ __forceinline__ float to_f(float x) { return x; }
+__device__ __forceinline__ float to_f(__half x) { return __half2float(x); }
+__device__ __forceinline__ float to_f(__nv_bfloat16 x) { return __bfloat162float(x); }
+template <class T>
+__device__ __forceinline__ T from_f(float x);
+template <>
+__device__ __forceinline__ float from_f<float>(float x) { return x; }
+template <>
+__device__ __forceinline__ __half from_f<__half>(float x) { return __float2half_rn(x); }
+template <>
+__device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) { return __float2bfloat16_rn(x); }
+
+// cos and sin of position p at F turns (2^-64) per position: p F wraps at
+// whole turns, so the product is exact; its top 32 bits are the angle in
+// (-1/2, 1/2] turns to 2^-32, under fp32's own rounding of it.
+__device__ __forceinline__ void turn(int p, int64_t F, float* c, float* s) {
+  const uint64_t phase = static_cast<uint64_t>(static_cast<int64_t>(p)) * static_cast<uint64_t>(F);
+  sincospif(static_cast<float>(static_cast<int32_t>(phase >> 32)) * 4.656612873077393e-10f /* 2^-31: half turns */, s, c);
+}
+
+// ------------------------------------------------------------------ sequences
+constexpr int kMaxLen = 0x7ffffc00;  // tokens of a sequence: positions and their roundings stay in 32 bits
+struct SeqItem {
+  int seq, local, row0, n;  // sequence (-1: none), item within it, its first row and its rows
+};
+// The sequence of work item `idx` when sequence s owns the items
+// [f(s), f(s + 1)), f(s) = (q_off[s] * mul >> shift) + add * s: a bound on its
+// tiles that needs no prefix sum.  A warp narrows 32 ways at a time.
+__device__ __forceinline__ SeqItem find_item(const SeqView& q, int idx, int mul, int shift, int add) {
+  const int lane = threadIdx.x & 31;
+  auto f = [&](int s) {
+    return static_cast<int>(static_cast<unsigned>(q.q_off[s]) * static_cast<unsigned>(mul) >> shift) + add * s;
+  };
+  int lo = 0, hi = q.n_seq;
+  do {
+    const int step = (hi - lo + 31) >> 5;
+    const int s = lo + lane * step;
+    const unsigned b = __ballot_sync(0xffffffffu, s < hi && f(s) <= idx);
+    if (b == 0) return SeqItem{-1, 0, 0, 0};
+    lo += (31 - __clz(b)) * step;
+    hi = min(hi, lo + step);
+  } while (hi - lo > 1);
+  SeqItem it;
+  it.seq = lo;
+  it.local = idx - f(lo);
+  it.row0 = q.q_off[lo];
+  it.n = q.q_off[lo + 1] - it.row0;
+  return it;
+}
+
+// ---------------------------------------------------------------------- codes
+constexpr float kScaleFloor = 8.673617379884035e-19f;  // 2^-60: a block of zeros has this scale
+
+// Scale of a block whose new rows reach |x| = am, beside `old` when older
+// tokens stay in it.  e4m3 scales are powers of two, so a grown scale moves
+// the older codes by whole exponents (exact while they stay normal).  A NaN
+// or infinity makes the scale so, and everything read from the block NaN.
+__device__ __forceinline__ float block_scale(float am, float old, bool held, int format) {
+  float need;
+  if (format == PCD_KV_INT8) {
+    need = am * (1.f / 127.f);
+  } else {
+    need = am * (1.f / 448.f);
+    if (isfinite(need)) need = __uint_as_float((__float_as_uint(need) + 0x7fffffu) & 0xff800000u);
+  }
+  if (need < kScaleFloor) need = kScaleFloor;
+  if (held && (old != old || need <= old)) return old;
+  return need;
+}
+__device__ __forceinline__ uint8_t encode(float x, int format) {
+  if (format == PCD_KV_INT8) return static_cast<uint8_t>(static_cast<int8_t>(max(-127, min(127, __float2int_rn(x)))));
+  return __nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3);
+}
+__device__ __forceinline__ float decode(uint8_t q, int format) {
+  if (format == PCD_KV_INT8) return static_cast<float>(static_cast<int8_t>(q));
+  return __half2float(__half(__nv_cvt_fp8_to_halfraw(q, __NV_E4M3)));
+}
+
+// Two codes in the upper bytes of a register's halves as fp16.  e4m3 shares
+// fp16's layout shifted by one bit, with a bias of 7 for 15: the halves hold
+// 2^-8 of the values, subnormals included.  (0x7f, its NaN, reads as 480: a
+// NaN shows in the block's scale instead.)
+__device__ __forceinline__ uint32_t fp8_half(uint32_t x) { return (x & 0x80008000u) | ((x >> 1) & 0x3f803f80u); }
+// int8 codes with the sign bit flipped, under the exponent of 1024.
+__device__ __forceinline__ uint32_t int8_half(uint32_t x) {
+  const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&x), __half2half2(__ushort_as_half(0x6480)));  // - 1152
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+// Codes 0, 1 and 2, 3 of a word.
+template <int FMT>
+__device__ __forceinline__ void codes4_half(uint32_t w, uint32_t* h0, uint32_t* h1) {
+  if constexpr (FMT == PCD_KV_E4M3) {
+    *h0 = fp8_half(__byte_perm(w, 0, 0x1404));
+    *h1 = fp8_half(__byte_perm(w, 0, 0x3424));
+  } else {
+    w ^= 0x80808080u;
+    *h0 = int8_half(__byte_perm(w, 0x64646464u, 0x4140));
+    *h1 = int8_half(__byte_perm(w, 0x64646464u, 0x4342));
+  }
+}
+// Code b of two words.
+template <int FMT>
+__device__ __forceinline__ uint32_t codes_pair_half(uint32_t w0, uint32_t w1, int b) {
+  if constexpr (FMT == PCD_KV_E4M3) {
+    return fp8_half(__byte_perm(w0, w1, (b << 4) | ((4 + b) << 12)));  // the lower bytes fall to fp8_half's masks
+  } else {
+    const uint32_t p = __byte_perm(w0, w1, b | ((4 + b) << 8));
+    return int8_half(((p ^ 0x00800080u) & 0x00ff00ffu) | 0x64006400u);
+  }
+}
+
+// ----------------------------------------------------------------------- rows
+__device__ __forceinline__ float lg2(float x) {
+  float y;
+  asm("lg2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// bf16 queries enter the fp16 products scaled by a power of two that takes the
+// row's largest |q| (bits am) to [2^14, 2^15): exact down to 2^-29 of it.
+// Returns the factor to undo it.
+template <class T>
+__device__ __forceinline__ float row_power(uint32_t am, float* down) {
+  int e = static_cast<int>(am >> 23);
+  if (std::is_same<T, __half>::value || e == 0 || e == 255) {
+    *down = 1.f;
+    return 1.f;
+  }
+  e = max(1, min(253, 127 + 14 + 127 - e));
+  *down = __uint_as_float(static_cast<uint32_t>(e) << 23);
+  return __uint_as_float(static_cast<uint32_t>(254 - e) << 23);
+}
+
+constexpr float kBias = 8.f;  // weights are exp2(x - M + kBias)
+
+// Partial softmax states of a row joined: reference M, sum L, 4 channels of O.
+struct RowState {
+  float M = -INFINITY, L = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  __device__ __forceinline__ void top(float2 ml) {
+    if (ml.y != 0.f) M = fmaxf(M, ml.x);
+  }
+  __device__ __forceinline__ void add(float2 ml, float4 v) {
+    if (ml.y == 0.f) return;
+    const float w = ex2_approx(ml.x - M);
+    L = fmaf(w, ml.y, L);
+    o.x = fmaf(w, v.x, o.x);
+    o.y = fmaf(w, v.y, o.y);
+    o.z = fmaf(w, v.z, o.z);
+    o.w = fmaf(w, v.w, o.w);
+  }
+};
+// Writes 4 channels of a row: the output, or the partial of key range z.
+template <class T>
+__device__ __forceinline__ void finish_row(const PagedAttnArgs& a, const RowState& st, int z, int tok, int hq, int d,
+                                           float unit) {
+  if (a.n_splits > 1) {
+    const int64_t row = (static_cast<int64_t>(z) * a.q.n_tok + tok) * a.Hq + hq;
+    if (d == 0) a.part_ml[row] = make_float2(st.M, st.L);
+    if (st.L != 0.f) *reinterpret_cast<float4*>(a.part_o + row * a.c.dim + d) = st.o;
+    return;
+  }
+  const float il = st.L == 0.f ? 0.f : unit / st.L;
+  T* out = static_cast<T*>(a.out) + tok * a.out_tok + hq * a.out_head + d;
+  out[0] = from_f<T>(st.o.x * il);
+  out[1] = from_f<T>(st.o.y * il);
+  out[2] = from_f<T>(st.o.z * il);
+  out[3] = from_f<T>(st.o.w * il);
+  if (a.lse && d == 0)
+    a.lse[static_cast<int64_t>(tok) * a.Hq + hq] =
+        st.L == 0.f ? -INFINITY : (st.M - kBias + log2f(st.L)) * 0.6931471805599453f;
+}
+
+}  // namespace pcd

@@ -1,0 +1,257 @@
+// extern "C" entry points of rotary positions and the 8-bit paged K/V cache
+// (include/pcd_kernels.h): argument checks, then one launch each.
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <climits>
+#include <cstdint>
+
+#include "paged.h"
+#include "pcd.h"
+#include "pcd_kernels.h"
+
+// Refuses the call with a code and pcd_last_error's text.
+#define PCD_REFUSE(cond, code, detail)                    \
+  do {                                                    \
+    if (cond) return pcd::set_error(code, detail);        \
+  } while (0)
+
+namespace {
+
+constexpr int64_t kMaxRows = int64_t{1} << 30;  // query rows (tokens x heads) of a call
+constexpr int kMaxSeqs = 1 << 24;
+
+int elem_size(int dtype) {
+  switch (dtype) {
+    case PCD_DTYPE_F32: return 4;
+    case PCD_DTYPE_F16:
+    case PCD_DTYPE_BF16: return 2;
+    default: return 0;
+  }
+}
+bool aligned(const void* p, int64_t n) { return reinterpret_cast<uintptr_t>(p) % static_cast<uintptr_t>(n) == 0; }
+
+int device_sms() {
+  int dev = 0, sms = 0;
+  cudaGetDevice(&dev);
+  cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  return sms > 0 ? sms : 1;
+}
+
+int launched(int r) {
+  if (r == 0) return PCD_OK;
+  const cudaError_t e = cudaGetLastError();
+  return pcd::set_error(PCD_ERR_CUDA, e == cudaSuccess ? "kernel launch failed" : cudaGetErrorString(e));
+}
+
+int check_rope(const pcd::RopeSpec& r, int dim) {
+  PCD_REFUSE(r.rot < 0 || r.rot % 2 || r.rot > dim, PCD_ERR_INVALID_ARG, "rot_dim is even and at most head_dim");
+  PCD_REFUSE((r.rot > 0) != (r.freqs != nullptr), PCD_ERR_INVALID_ARG, "freqs go with rot_dim > 0");
+  PCD_REFUSE(!aligned(r.freqs, 8), PCD_ERR_INVALID_ARG, "freqs: unaligned pointer");
+  PCD_REFUSE(!std::isfinite(r.amp), PCD_ERR_INVALID_ARG, "amp is not finite");
+  return PCD_OK;
+}
+
+int log2_page(int page) {
+  for (int s = 4; s <= 7; ++s)
+    if (page == 1 << s) return s;
+  return -1;
+}
+
+// The cache as the kernels take it.
+int view_pages(const pcd_kv_pages* c, pcd::PagesView* v) {
+  PCD_REFUSE(!c || !c->k || !c->v || !c->k_scale || !c->v_scale, PCD_ERR_INVALID_ARG, "cache: NULL");
+  const int shift = log2_page(c->page_size);
+  PCD_REFUSE(shift < 0, PCD_ERR_INVALID_ARG, "page_size is 16, 32, 64 or 128");
+  PCD_REFUSE(c->n_pages < 1 || c->n_kv_heads < 1 || c->n_kv_heads > 65535, PCD_ERR_INVALID_ARG,
+             "cache: pages or KV heads out of range");
+  PCD_REFUSE(c->format != PCD_KV_E4M3 && c->format != PCD_KV_INT8, PCD_ERR_INVALID_ARG, "cache: unknown format");
+  PCD_REFUSE(c->head_dim != 64 && c->head_dim != 128, PCD_ERR_SHAPE_MISMATCH, "cache: head_dim is 64 or 128");
+  const int64_t tok = c->token_stride, head = c->head_stride, page = c->page_stride;
+  PCD_REFUSE(!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4) ||
+                 page % 16 || head % 16 || tok % 16,
+             PCD_ERR_INVALID_ARG, "cache: rows of codes start at multiples of 16 bytes");
+  PCD_REFUSE(tok < c->head_dim || (c->n_kv_heads > 1 && head < c->head_dim) || (c->n_pages > 1 && page < c->head_dim),
+             PCD_ERR_INVALID_ARG, "cache: strides overlap rows");
+  *v = pcd::PagesView{static_cast<uint8_t*>(c->k), static_cast<uint8_t*>(c->v), c->k_scale, c->v_scale, page, head, tok,
+                      c->n_pages, shift, c->n_kv_heads, c->head_dim, c->format};
+  return PCD_OK;
+}
+
+int view_seqs(const int32_t* q_off, const int32_t* kv_len, const int32_t* table, int n_seq, int n_tok, int table_stride,
+              pcd::SeqView* v) {
+  PCD_REFUSE(n_seq < 0 || n_tok < 0 || table_stride < 0 || n_seq > kMaxSeqs || n_tok > kMaxRows, PCD_ERR_INVALID_ARG,
+             "sequences, rows or table width out of range");
+  PCD_REFUSE(n_seq > 0 && (!q_off || !kv_len || (table_stride > 0 && !table)), PCD_ERR_INVALID_ARG,
+             "q_off, kv_len or table: NULL");
+  PCD_REFUSE(!aligned(q_off, 4) || !aligned(kv_len, 4) || !aligned(table, 4), PCD_ERR_INVALID_ARG,
+             "q_off, kv_len or table: unaligned pointer");
+  *v = pcd::SeqView{q_off, kv_len, table, n_seq, n_tok, table_stride};
+  return PCD_OK;
+}
+
+// May a kernel that reads x and writes y element by element in place of the
+// other run on these two views?
+bool rope_overlap_ok(const void* x, const void* y, int64_t es, int n, int h, int d, int64_t xt, int64_t xh, int64_t yt,
+                     int64_t yh) {
+  if (x == y && (xt == yt || n <= 1) && (xh == yh || h <= 1)) return true;
+  const int64_t xa = reinterpret_cast<int64_t>(x), ya = reinterpret_cast<int64_t>(y);
+  const int64_t xs = ((n - 1) * xt + (h - 1) * xh + d) * es, ys = ((n - 1) * yt + (h - 1) * yh + d) * es;
+  if (xa + xs <= ya || ya + ys <= xa) return true;
+  if (xt != yt || xt <= 0) return false;
+  // rows interleave: side by side within the common token stride
+  const int64_t row = xt * es, xr = ((h - 1) * xh + d) * es, yr = ((h - 1) * yh + d) * es;
+  int64_t off = (ya - xa) % row;
+  if (off < 0) off += row;
+  return off >= xr && off + yr <= row;
+}
+
+}  // namespace
+
+extern "C" int pcd_rope_freqs(int rot_dim, double theta, int scaling, double factor, double orig_len, double lo_turns,
+                              double hi_turns, int64_t* freqs, float* amp) {
+  PCD_REFUSE(rot_dim < 2 || rot_dim % 2 || !freqs, PCD_ERR_INVALID_ARG, "rot_dim is even and at least 2");
+  PCD_REFUSE(!(theta > 1.0) || !std::isfinite(theta), PCD_ERR_INVALID_ARG, "theta is over 1");
+  PCD_REFUSE(scaling < PCD_ROPE_NONE || scaling > PCD_ROPE_RAMP, PCD_ERR_INVALID_ARG, "unknown scaling");
+  PCD_REFUSE(scaling != PCD_ROPE_NONE && (!(factor >= 1.0) || !std::isfinite(factor)), PCD_ERR_INVALID_ARG,
+             "factor is at least 1");
+  PCD_REFUSE(scaling == PCD_ROPE_BASE && rot_dim < 4, PCD_ERR_INVALID_ARG, "PCD_ROPE_BASE needs rot_dim >= 4");
+  PCD_REFUSE(scaling >= PCD_ROPE_BANDS && (!(orig_len >= 1.0) || !std::isfinite(orig_len) || !(lo_turns > 0.0) ||
+                                           !(hi_turns > lo_turns) || !std::isfinite(hi_turns)),
+             PCD_ERR_INVALID_ARG, "orig_len >= 1 and 0 < lo_turns < hi_turns");
+  constexpr double kTwoPi = 6.283185307179586476925286766559;
+  double base = theta;
+  if (scaling == PCD_ROPE_BASE) base *= std::pow(factor, rot_dim / (rot_dim - 2.0));
+  double lo = 0.0, hi = 0.0;
+  if (scaling == PCD_ROPE_RAMP) {
+    // pair index at which a pair turns `t` times over the original length
+    auto at = [&](double t) { return rot_dim * std::log(orig_len / (t * kTwoPi)) / (2.0 * std::log(theta)); };
+    lo = std::fmax(std::floor(at(hi_turns)), 0.0);
+    hi = std::fmin(std::ceil(at(lo_turns)), rot_dim - 1.0);
+  }
+  for (int i = 0; i < rot_dim / 2; ++i) {
+    const double f0 = std::pow(base, -2.0 * i / rot_dim);
+    double stretched = 0.0;  // share of the pair that takes the divided frequency
+    if (scaling == PCD_ROPE_LINEAR) {
+      stretched = 1.0;
+    } else if (scaling == PCD_ROPE_BANDS) {
+      const double turns = orig_len * f0 / kTwoPi;
+      stretched = 1.0 - std::fmin(std::fmax((turns - lo_turns) / (hi_turns - lo_turns), 0.0), 1.0);
+    } else if (scaling == PCD_ROPE_RAMP) {
+      stretched = std::fmin(std::fmax((i - lo) / std::fmax(hi - lo, 1e-3), 0.0), 1.0);
+    }
+    const double f = stretched > 0.0 ? f0 / factor * stretched + f0 * (1.0 - stretched) : f0;
+    const double turns = f / kTwoPi;  // < 1/6: theta > 1 and factor >= 1
+    freqs[i] = static_cast<int64_t>(static_cast<uint64_t>(std::ldexp(turns, 64)));
+  }
+  if (amp) *amp = scaling == PCD_ROPE_RAMP ? static_cast<float>(0.1 * std::log(factor) + 1.0) : 1.f;
+  return PCD_OK;
+}
+
+extern "C" int pcd_k_rope(const void* x, void* y, int dtype, int n_tok, int heads, int head_dim, int64_t x_tok,
+                          int64_t x_head, int64_t y_tok, int64_t y_head, const int64_t* freqs, int rot_dim,
+                          int interleaved, float amp, const int32_t* pos, int base, int transpose, void* stream) {
+  const int es = elem_size(dtype);
+  PCD_REFUSE(!es, PCD_ERR_INVALID_ARG, "unknown dtype");
+  PCD_REFUSE(n_tok < 0 || heads < 0 || head_dim < 1 || head_dim > 1024, PCD_ERR_INVALID_ARG, "sizes out of range");
+  pcd::RopeKArgs a{x, y, dtype, n_tok, heads, head_dim, x_tok, x_head, y_tok, y_head, {}, pos, base};
+  a.rope = pcd::RopeSpec{freqs, rot_dim, interleaved != 0, amp, transpose != 0};
+  const int rc = check_rope(a.rope, head_dim);
+  if (rc != PCD_OK) return rc;
+  if (n_tok == 0 || heads == 0) return PCD_OK;
+  PCD_REFUSE(!x || !y || !aligned(x, es) || !aligned(y, es) || !aligned(pos, 4), PCD_ERR_INVALID_ARG,
+             "NULL or unaligned pointer");
+  PCD_REFUSE(x_tok < 0 || x_head < 0 || y_tok < 0 || y_head < 0, PCD_ERR_INVALID_ARG, "negative stride");
+  PCD_REFUSE((heads > 1 && y_head < head_dim) || (n_tok > 1 && y_tok < head_dim), PCD_ERR_INVALID_ARG,
+             "strides of y overlap rows");
+  PCD_REFUSE(!rope_overlap_ok(x, y, es, n_tok, heads, head_dim, x_tok, x_head, y_tok, y_head), PCD_ERR_INVALID_ARG,
+             "x and y overlap without being the same view");
+  PCD_REFUSE(static_cast<int64_t>(n_tok) * heads * head_dim >= (int64_t{1} << 38), PCD_ERR_INVALID_ARG, "too large");
+  return launched(pcd::launch_rope(a, static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" int pcd_k_kv_append(const pcd_kv_pages* cache, const void* k, const void* v, int dtype, int64_t k_tok,
+                               int64_t k_head, int64_t v_tok, int64_t v_head, const int32_t* q_off,
+                               const int32_t* kv_len, const int32_t* table, int n_seq, int n_tok, int table_stride,
+                               const int64_t* freqs, int rot_dim, int interleaved, float amp, const int32_t* pos,
+                               int* dev_err, void* stream) {
+  pcd::AppendArgs a{};
+  int rc = view_pages(cache, &a.c);
+  if (rc == PCD_OK) rc = view_seqs(q_off, kv_len, table, n_seq, n_tok, table_stride, &a.q);
+  if (rc != PCD_OK) return rc;
+  const int es = elem_size(dtype);
+  PCD_REFUSE(!es, PCD_ERR_INVALID_ARG, "unknown dtype");
+  a.rope = pcd::RopeSpec{freqs, rot_dim, interleaved != 0, amp, 0};
+  rc = check_rope(a.rope, a.c.dim);
+  if (rc != PCD_OK) return rc;
+  if (n_tok == 0 || n_seq == 0) return PCD_OK;
+  PCD_REFUSE(!k || !v || !aligned(k, es) || !aligned(v, es) || !aligned(pos, 4) || !aligned(dev_err, 4),
+             PCD_ERR_INVALID_ARG, "NULL or unaligned pointer");
+  PCD_REFUSE(k_tok < 0 || k_head < 0 || v_tok < 0 || v_head < 0, PCD_ERR_INVALID_ARG, "negative stride");
+  a.k = k;
+  a.v = v;
+  a.dtype = dtype;
+  a.k_tok = k_tok, a.k_head = k_head, a.v_tok = v_tok, a.v_head = v_head;
+  a.pos = pos;
+  a.err = dev_err;
+  return launched(pcd::launch_kv_append(a, static_cast<cudaStream_t>(stream)));
+}
+
+namespace {
+int64_t attn_scratch(int n_tok, int Hq, int dim, int n_splits) {
+  if (n_splits <= 1) return 0;
+  return static_cast<int64_t>(n_splits) * n_tok * Hq * (dim * 4 + 8);
+}
+}  // namespace
+
+extern "C" int64_t pcd_k_paged_attention_scratch_bytes(int n_tok, int n_seq, int n_q_heads, int n_kv_heads, int head_dim,
+                                                       int64_t max_kv) {
+  if (n_tok < 1 || n_seq < 1 || n_q_heads < 1 || n_kv_heads < 1 || n_q_heads % n_kv_heads || head_dim < 1 || max_kv < 0 ||
+      static_cast<int64_t>(n_tok) * n_q_heads > kMaxRows)
+    return 0;
+  int n_splits = 1, split_len = 0;
+  pcd::plan_paged_attention(n_tok, n_seq, n_q_heads / n_kv_heads, n_kv_heads, head_dim, max_kv, device_sms(), &n_splits,
+                            &split_len);
+  return attn_scratch(n_tok, n_q_heads, head_dim, n_splits);
+}
+
+extern "C" int pcd_k_paged_attention(const pcd_kv_pages* cache, const void* q, void* out, float* lse, int dtype,
+                                     int n_q_heads, int64_t q_tok, int64_t q_head, int64_t out_tok, int64_t out_head,
+                                     const int32_t* q_off, const int32_t* kv_len, const int32_t* table, int n_seq,
+                                     int n_tok, int table_stride, int64_t max_kv, int causal, float scale, void* scratch,
+                                     int64_t scratch_bytes, int* dev_err, void* stream) {
+  pcd::PagedAttnArgs a{};
+  int rc = view_pages(cache, &a.c);
+  if (rc == PCD_OK) rc = view_seqs(q_off, kv_len, table, n_seq, n_tok, table_stride, &a.q);
+  if (rc != PCD_OK) return rc;
+  PCD_REFUSE(dtype != PCD_DTYPE_F16 && dtype != PCD_DTYPE_BF16, PCD_ERR_INVALID_ARG, "queries are fp16 or bf16");
+  PCD_REFUSE(n_q_heads < 1 || n_q_heads % a.c.Hkv || n_q_heads / a.c.Hkv > 128, PCD_ERR_INVALID_ARG,
+             "query heads are 1 to 128 times the KV heads");
+  PCD_REFUSE(!(scale > 0.f) || !std::isfinite(scale) || max_kv < 0, PCD_ERR_INVALID_ARG, "scale or max_kv out of range");
+  PCD_REFUSE(static_cast<int64_t>(n_tok) * n_q_heads > kMaxRows, PCD_ERR_INVALID_ARG, "too many query rows");
+  if (n_tok == 0 || n_seq == 0) return PCD_OK;
+  PCD_REFUSE(!q || !out || !aligned(q, 2) || !aligned(out, 2) || !aligned(lse, 4) || !aligned(dev_err, 4),
+             PCD_ERR_INVALID_ARG, "NULL or unaligned pointer");
+  PCD_REFUSE(q_tok < 0 || q_head < 0 || out_tok < 0 || out_head < 0, PCD_ERR_INVALID_ARG, "negative stride");
+  PCD_REFUSE((n_q_heads > 1 && out_head < a.c.dim) || (n_tok > 1 && out_tok < a.c.dim), PCD_ERR_INVALID_ARG,
+             "strides of out overlap rows");
+  a.x = q;
+  a.out = out;
+  a.lse = lse;
+  a.dtype = dtype;
+  a.Hq = n_q_heads;
+  a.G = n_q_heads / a.c.Hkv;
+  a.causal = causal != 0;
+  a.x_tok = q_tok, a.x_head = q_head, a.out_tok = out_tok, a.out_head = out_head;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  a.err = dev_err;
+  pcd::plan_paged_attention(n_tok, n_seq, a.G, a.c.Hkv, a.c.dim, max_kv, device_sms(), &a.n_splits, &a.split_len);
+  const int64_t need = attn_scratch(n_tok, n_q_heads, a.c.dim, a.n_splits);
+  if (need > 0) {
+    PCD_REFUSE(!scratch || !aligned(scratch, 16) || scratch_bytes < need, PCD_ERR_INVALID_ARG,
+               "scratch is smaller than pcd_k_paged_attention_scratch_bytes, or unaligned");
+    a.part_o = static_cast<float*>(scratch);
+    a.part_ml = reinterpret_cast<float2*>(a.part_o + static_cast<int64_t>(a.n_splits) * n_tok * n_q_heads * a.c.dim);
+  }
+  return launched(pcd::launch_paged_attention(a, static_cast<cudaStream_t>(stream)));
+}

@@ -143,6 +143,121 @@ int pcd_plan_inspect(const void* fields, int n_fields, int vocab, int32_t* sizes
  * line's length, or PCD_ERR_INVALID_ARG when no path spells the label. */
 int pcd_answer_line(const void* field, int label, const int32_t* sep, int n_sep, int32_t* out, int cap);
 
+/* ------------------------------------------------- rotary positions, paged cache
+ * The calls below serve many requests over one pool of cache pages, beside
+ * the contiguous caches of pcd.h: rotate the queries (pcd_k_rope), store the
+ * new keys and values (pcd_k_kv_append), attend (pcd_k_paged_attention).  They
+ * follow the conventions above: device pointers, no allocation, no
+ * synchronisation, and they may be captured into CUDA graphs.  What they find
+ * wrong in device arrays (offsets, lengths, pages out of range) is skipped
+ * and recorded as a nonzero code in `dev_err` (device int, may be NULL).
+ * pcd_last_error() says why a call was refused. */
+#define PCD_DTYPE_F16 3 /* beside PCD_DTYPE_F32 and PCD_DTYPE_BF16 of pcd.h */
+
+/* Frequencies of rotary positions.  Pair i of the rot_dim / 2 pairs turns by
+ * f_i = theta^(-2i / rot_dim) radians a position, changed for contexts longer
+ * than the trained orig_len by
+ *   PCD_ROPE_LINEAR  f_i / factor;
+ *   PCD_ROPE_BASE    theta grown by factor^(rot_dim / (rot_dim - 2));
+ *   PCD_ROPE_BANDS   pairs that turn at least hi_turns times over orig_len
+ *                    stay, those under lo_turns are divided by factor, a
+ *                    blend linear in their turns between;
+ *   PCD_ROPE_RAMP    the same ends with a ramp linear in the pair's index,
+ *                    between the indices where pairs turn hi_turns and
+ *                    lo_turns times (rounded outwards); cos and sin are
+ *                    multiplied by 0.1 ln(factor) + 1.
+ * factor >= 1; orig_len and the turns are read by the last two only.  Writes
+ * rot_dim / 2 HOST values: f_i as a fraction of a turn in units of 2^-64, so
+ * that a position's angle is one wrapping integer product, exact at any int32
+ * position; the caller copies them to the device.  `amp` (may be NULL)
+ * receives the factor on cos and sin. */
+#define PCD_ROPE_NONE 0
+#define PCD_ROPE_LINEAR 1
+#define PCD_ROPE_BASE 2
+#define PCD_ROPE_BANDS 3
+#define PCD_ROPE_RAMP 4
+int pcd_rope_freqs(int rot_dim, double theta, int scaling, double factor, double orig_len, double lo_turns,
+                   double hi_turns, int64_t* freqs, float* amp);
+
+/* Rotates the first rot_dim channels of every head of x [n_tok][heads]
+ * [head_dim] into y (the other channels are copied; rot_dim 0 with freqs NULL
+ * copies all).  dtype: PCD_DTYPE_F32, _F16 or _BF16 for both; arithmetic in
+ * fp32, one rounding.  Strides of tokens and heads in elements, channels
+ * contiguous.  Pair (a, b) at angle phi becomes amp (a cos phi - b sin phi,
+ * b cos phi + a sin phi); pairs are channels (2i, 2i + 1) when `interleaved`,
+ * else (i, i + rot_dim / 2).  transpose != 0 turns by -phi with the same amp:
+ * the gradient of the rotation.  Token t is at pos[t], or base + t when pos is
+ * NULL; any int32 position, negative ones included.  y may be x's own view;
+ * another overlap is refused. */
+int pcd_k_rope(const void* x, void* y, int dtype, int n_tok, int heads, int head_dim, int64_t x_tok, int64_t x_head,
+               int64_t y_tok, int64_t y_head, const int64_t* freqs, int rot_dim, int interleaved, float amp,
+               const int32_t* pos, int base, int transpose, void* stream);
+
+/* A pool of cache pages in 8 bits.  The K and V codes of (page, KV head, slot)
+ * are head_dim bytes at page * page_stride + head * head_stride + slot *
+ * token_stride of `k` and `v` (strides and bases multiples of 16 bytes), so
+ * both [page][head][slot] and [page][slot][head] orders serve.  A page holds
+ * page_size (16, 32, 64 or 128) consecutive tokens of one sequence; each
+ * (page, KV head) has one scale in k_scale / v_scale [n_pages][n_kv_heads],
+ * fp32: value = code * scale.  head_dim 64 or 128. */
+#define PCD_KV_E4M3 1 /* 8-bit floats, 4 exponent bits; scales are powers of two when written here */
+#define PCD_KV_INT8 2 /* signed integers, -127 .. 127 */
+typedef struct {
+  void *k, *v;
+  float *k_scale, *v_scale;
+  int64_t page_stride, head_stride, token_stride;
+  int n_pages, page_size, n_kv_heads, head_dim, format;
+} pcd_kv_pages;
+
+/* Both calls below take ragged sequences: rows q_off[s] .. q_off[s + 1) of
+ * the n_tok rows belong to sequence s (n_seq + 1 non-decreasing offsets; a
+ * sequence may have none, and rows behind the last offset are left alone),
+ * kv_len[s] counts the sequence's tokens in the cache with the new ones
+ * included, and token j of it lies in page table[s * table_stride + j /
+ * page_size], slot j % page_size.
+ *
+ * Append: the n new tokens of sequence s become its tokens kv_len[s] - n ..
+ * kv_len[s] - 1.  k, v [n_tok][n_kv_heads][head_dim] of `dtype` (strides in
+ * elements, channels contiguous).  Keys are rotated first, as by pcd_k_rope,
+ * at pos[row] or, when pos is NULL, at their place in the sequence; freqs NULL
+ * with rot_dim 0 stores them as they are.  A page's scale is set by its new
+ * rows' largest |x|: over 448 rounded up to a power of two (e4m3) or over 127
+ * (int8), at least 2^-60; while older tokens of the sequence stay in the
+ * page it only grows, and their codes are then rescaled (e4m3: by a power of
+ * two, exact while they stay normal; int8: rounded once more).  Codes round to
+ * nearest even.  A NaN or infinity in a block's rows makes its scale so, and
+ * all that is read from that block NaN.  A page that one call appends to
+ * belongs to one sequence.  Nothing but the new tokens' pages is written. */
+int pcd_k_kv_append(const pcd_kv_pages* cache, const void* k, const void* v, int dtype, int64_t k_tok, int64_t k_head,
+                    int64_t v_tok, int64_t v_head, const int32_t* q_off, const int32_t* kv_len, const int32_t* table,
+                    int n_seq, int n_tok, int table_stride, const int64_t* freqs, int rot_dim, int interleaved,
+                    float amp, const int32_t* pos, int* dev_err, void* stream);
+
+/* Attention of q [n_tok][n_q_heads][head_dim] (dtype PCD_DTYPE_F16 or _BF16)
+ * over the cache: out = softmax(scale q k^T) v per query head, query head h
+ * reading KV head h / (n_q_heads / n_kv_heads).  causal != 0: row i of the n of
+ * sequence s is its token kv_len[s] - n + i and sees the tokens up to itself
+ * (rows before the cache's first token see none); causal == 0: every row sees
+ * all kv_len[s] tokens, as branch rows see their shared prefix (How TypeSafe's
+ * Jev Might Work, "One forward pass for all fields").  `lse` (may be NULL)
+ * [n_tok][n_q_heads] fp32 receives the natural log-sum-exp of the scaled
+ * scores, to join the result with attention over other keys.  A row that sees
+ * nothing gives zeros and -inf.  Scores, softmax sums and the output are
+ * accumulated in fp32; codes enter the products exactly and a value's scale
+ * joins the softmax weight before its rounding to fp16.  Keys of a page that
+ * the table has out of range are not seen; a length beyond the table reads as
+ * zero tokens.  max_kv: the longest kv_len, as far as the host knows it; it
+ * sets how many key ranges run side by side, not what is computed.  `scratch`: 16-byte aligned, at least
+ * pcd_k_paged_attention_scratch_bytes (the same sizes, the same GPU) bytes
+ * that the call overwrites; calls that may overlap need their own. */
+int64_t pcd_k_paged_attention_scratch_bytes(int n_tok, int n_seq, int n_q_heads, int n_kv_heads, int head_dim,
+                                            int64_t max_kv);
+int pcd_k_paged_attention(const pcd_kv_pages* cache, const void* q, void* out, float* lse, int dtype, int n_q_heads,
+                          int64_t q_tok, int64_t q_head, int64_t out_tok, int64_t out_head, const int32_t* q_off,
+                          const int32_t* kv_len, const int32_t* table, int n_seq, int n_tok, int table_stride,
+                          int64_t max_kv, int causal, float scale, void* scratch, int64_t scratch_bytes, int* dev_err,
+                          void* stream);
+
 #ifdef __cplusplus
 }
 #endif
