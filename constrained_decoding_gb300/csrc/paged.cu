@@ -240,8 +240,8 @@ __global__ void __launch_bounds__(kWarps * 32, 3) paged_attn_rows_kernel(PagedAt
   auto seen = [&](int r) { return a.causal ? first + min(r, R - 1) / a.G : len; };
   const int kmax = max(0, seen(r_end - 1));
   const int kmin = max(0, seen(r0));
-  const int b0 = z * (a.split_len >> 4);
-  const int b1 = z + 1 < a.n_splits ? min((kmax + 15) >> 4, b0 + (a.split_len >> 4)) : (kmax + 15) >> 4;
+  const int b0 = z * (a.plan.split_len >> 4);
+  const int b1 = z + 1 < a.plan.n_splits ? min((kmax + 15) >> 4, b0 + (a.plan.split_len >> 4)) : (kmax + 15) >> 4;
   const int nb = b1 > b0 + warp ? (b1 - b0 - warp + kWarps - 1) / kWarps : 0;  // blocks of this warp
 
   // ---- Q fragments: k-step t takes channels (64 * (t / 4) + 16 c + 4 (t % 4)) + {0, 1 | 2, 3}
@@ -374,8 +374,9 @@ __global__ void __launch_bounds__(kWarps * 32, 3) paged_attn_rows_kernel(PagedAt
     // ---- weights
     const int j0 = block_at(i) << 4;
     const float lsv = lg2(bsv);
-    const float isv = 1.f / bsv;
     const bool bad = bsv == -1.f;  // a page the table has wrong: nothing of it is seen
+    // a poisoned scale (NaN) counts only for rows that see its keys
+    const float iv[2] = {bad || vis[0] <= j0 ? 0.f : 1.f / bsv, bad || vis[1] <= j0 ? 0.f : 1.f / bsv};
     float ak[2];
     ak[0] = qs[0] * bsk;
     ak[1] = qs[1] * bsk;
@@ -423,7 +424,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) paged_attn_rows_kernel(PagedAt
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         s[t][e] = ex2_approx(s[t][e] - mb[e >> 1]);
-        row_l[e >> 1] = fmaf(s[t][e], bad ? 0.f : isv, row_l[e >> 1]);
+        row_l[e >> 1] = fmaf(s[t][e], iv[e >> 1], row_l[e >> 1]);
       }
     const uint32_t pf[4] = {pack2(s[0][0], s[0][1]), pack2(s[0][2], s[0][3]), pack2(s[1][0], s[1][1]),
                             pack2(s[1][2], s[1][3])};
@@ -499,14 +500,14 @@ __global__ void __launch_bounds__(256) paged_attn_join_kernel(PagedAttnArgs a, f
   const int tok = static_cast<int>(row / a.Hq), hq = static_cast<int>(row % a.Hq);
   if (tok < a.q.q_off[0] || tok >= a.q.q_off[a.q.n_seq]) return;  // rows of no sequence stay as they are
   RowState st;
-  for (int z = 0; z < a.n_splits; ++z) st.top(a.part_ml[z * rows + row]);
-  for (int z = 0; z < a.n_splits; ++z) {
+  for (int z = 0; z < a.plan.n_splits; ++z) st.top(a.part_ml[z * rows + row]);
+  for (int z = 0; z < a.plan.n_splits; ++z) {
     const float2 ml = a.part_ml[z * rows + row];
     if (ml.y == 0.f) continue;
     st.add(ml, *reinterpret_cast<const float4*>(a.part_o + (z * rows + row) * D + d));
   }
   PagedAttnArgs b = a;
-  b.n_splits = 1;
+  b.plan.n_splits = 1;
   finish_row<T>(b, st, 0, tok, hq, d, unit);
 }
 
@@ -517,12 +518,8 @@ int launch_rows(const PagedAttnArgs& a, cudaStream_t s) {
   cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (r != cudaSuccess) return r;
   const int64_t items = ((static_cast<int64_t>(a.q.n_tok) * a.G) >> 4) + a.q.n_seq;
-  r = launch_k(kern, dim3(static_cast<unsigned>(items), static_cast<unsigned>(a.c.Hkv), static_cast<unsigned>(a.n_splits)),
-               dim3(kWarps * 32), C::kSmem, s, a);
-  if (r != cudaSuccess || a.n_splits == 1) return r;
-  const int64_t rows = static_cast<int64_t>(a.q.n_tok) * a.Hq;
-  return launch_k(paged_attn_join_kernel<D, T>, dim3(static_cast<unsigned>((rows * (D / 4) + 255) / 256)), dim3(256), 0, s, a,
-                  FMT == PCD_KV_E4M3 ? 256.f : 1.f);
+  return launch_k(kern, dim3(static_cast<unsigned>(items), static_cast<unsigned>(a.c.Hkv), static_cast<unsigned>(a.plan.n_splits)),
+                  dim3(kWarps * 32), C::kSmem, s, a);
 }
 
 template <int D, int FMT>
@@ -532,23 +529,39 @@ int launch_rows_t(const PagedAttnArgs& a, cudaStream_t s) {
 
 }  // namespace
 
-void plan_paged_attention(int n_tok, int n_seq, int G, int Hkv, int dim, int64_t max_kv, int sms, int* n_splits,
-                          int* split_len) {
-  const int64_t per = n_seq > 0 ? (n_tok + n_seq - 1) / n_seq : 0;
-  const int64_t tiles = std::max<int64_t>(1, n_seq * ((per * G + 15) / 16) * Hkv);
-  int64_t want = std::max<int64_t>(1, (static_cast<int64_t>(sms) * 12 + tiles - 1) / tiles);
-  want = std::min<int64_t>(want, 256);
+void plan_paged_attention(int n_tok, int n_seq, int G, int Hkv, int64_t max_kv, int sms, PagedPlan* p) {
+  const int64_t per = n_seq > 0 ? (n_tok + n_seq - 1) / n_seq : 0;  // query tokens of a sequence, on average
+  p->rows = per * G > 32 ? 256 : 16;
+  const int64_t tiles = std::max<int64_t>(1, n_seq * ((per * G + p->rows - 1) / p->rows) * Hkv);
+  const int64_t unit = p->rows == 16 ? 64 : 128;  // keys that a range is a multiple of
+  int64_t want = p->rows == 16 ? (static_cast<int64_t>(sms) * 12 + tiles - 1) / tiles : sms / tiles;
+  want = std::min<int64_t>(std::max<int64_t>(want, 1), 256);
   int64_t len = (max_kv + want - 1) / want;
-  len = std::max<int64_t>(64, (len + 63) / 64 * 64);
-  *split_len = static_cast<int>(std::min<int64_t>(len, 1 << 30));
-  *n_splits = static_cast<int>(std::max<int64_t>(1, (max_kv + len - 1) / len));
+  len = std::max<int64_t>(unit, (len + unit - 1) / unit * unit);
+  p->split_len = static_cast<int>(std::min<int64_t>(len, 1 << 30));
+  p->n_splits = static_cast<int>(std::max<int64_t>(1, (max_kv + len - 1) / len));
 }
 
 int launch_paged_attention(const PagedAttnArgs& a, cudaStream_t s) {
   if (a.q.n_tok == 0 || a.q.n_seq == 0) return 0;
   const bool f8 = a.c.format == PCD_KV_E4M3;
-  if (a.c.dim == 64) return f8 ? launch_rows_t<64, PCD_KV_E4M3>(a, s) : launch_rows_t<64, PCD_KV_INT8>(a, s);
-  return f8 ? launch_rows_t<128, PCD_KV_E4M3>(a, s) : launch_rows_t<128, PCD_KV_INT8>(a, s);
+  int r;
+  if (a.plan.rows == 256)
+    r = launch_paged_attention_tiles(a, s);
+  else if (a.c.dim == 64)
+    r = f8 ? launch_rows_t<64, PCD_KV_E4M3>(a, s) : launch_rows_t<64, PCD_KV_INT8>(a, s);
+  else
+    r = f8 ? launch_rows_t<128, PCD_KV_E4M3>(a, s) : launch_rows_t<128, PCD_KV_INT8>(a, s);
+  if (r != 0 || a.plan.n_splits == 1) return r;
+  const float unit = f8 ? 256.f : 1.f;
+  const int64_t threads = static_cast<int64_t>(a.q.n_tok) * a.Hq * (a.c.dim / 4);
+  const dim3 grid(static_cast<unsigned>((threads + 255) / 256));
+  const bool bf = a.dtype == PCD_DTYPE_BF16;
+  if (a.c.dim == 64)
+    return bf ? launch_k(paged_attn_join_kernel<64, __nv_bfloat16>, grid, dim3(256), 0, s, a, unit)
+              : launch_k(paged_attn_join_kernel<64, __half>, grid, dim3(256), 0, s, a, unit);
+  return bf ? launch_k(paged_attn_join_kernel<128, __nv_bfloat16>, grid, dim3(256), 0, s, a, unit)
+            : launch_k(paged_attn_join_kernel<128, __half>, grid, dim3(256), 0, s, a, unit);
 }
 
 }  // namespace pcd

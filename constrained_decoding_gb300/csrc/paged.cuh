@@ -168,7 +168,7 @@ struct RowState {
 template <class T>
 __device__ __forceinline__ void finish_row(const PagedAttnArgs& a, const RowState& st, int z, int tok, int hq, int d,
                                            float unit) {
-  if (a.n_splits > 1) {
+  if (a.plan.n_splits > 1) {
     const int64_t row = (static_cast<int64_t>(z) * a.q.n_tok + tok) * a.Hq + hq;
     if (d == 0) a.part_ml[row] = make_float2(st.M, st.L);
     if (st.L != 0.f) *reinterpret_cast<float4*>(a.part_o + row * a.c.dim + d) = st.o;

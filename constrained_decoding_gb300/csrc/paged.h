@@ -58,6 +58,12 @@ struct AppendArgs {
 };
 int launch_kv_append(const AppendArgs& a, cudaStream_t s);
 
+// How a call is cut up: query rows of a work item (16: warp MMA, 256:
+// tcgen05) and key ranges of split_len, the last taking the rest.
+struct PagedPlan {
+  int rows, n_splits, split_len;
+};
+
 struct PagedAttnArgs {
   PagesView c;
   SeqView q;
@@ -67,14 +73,13 @@ struct PagedAttnArgs {
   int dtype, Hq, G, causal;
   int64_t x_tok, x_head, out_tok, out_head;  // elements
   float scale_log2;                          // softmax scale x log2(e)
-  int n_splits, split_len;                   // key ranges of split_len (a multiple of 64); the last takes the rest
-  float* part_o;                             // [n_splits][n_tok][Hq][dim], n_splits > 1
+  PagedPlan plan;
+  float* part_o;                             // [n_splits][n_tok][Hq][dim], plan.n_splits > 1
   float2* part_ml;                           // [n_splits][n_tok][Hq]
   int* err;
 };
-// Key ranges for a call of these sizes.
-void plan_paged_attention(int n_tok, int n_seq, int G, int Hkv, int dim, int64_t max_kv, int sms, int* n_splits,
-                          int* split_len);
+void plan_paged_attention(int n_tok, int n_seq, int G, int Hkv, int64_t max_kv, int sms, PagedPlan* p);
 int launch_paged_attention(const PagedAttnArgs& a, cudaStream_t s);
+int launch_paged_attention_tiles(const PagedAttnArgs& a, cudaStream_t s);  // plan.rows == 256, without the join
 
 }  // namespace pcd

@@ -209,10 +209,9 @@ extern "C" int64_t pcd_k_paged_attention_scratch_bytes(int n_tok, int n_seq, int
   if (n_tok < 1 || n_seq < 1 || n_q_heads < 1 || n_kv_heads < 1 || n_q_heads % n_kv_heads || head_dim < 1 || max_kv < 0 ||
       static_cast<int64_t>(n_tok) * n_q_heads > kMaxRows)
     return 0;
-  int n_splits = 1, split_len = 0;
-  pcd::plan_paged_attention(n_tok, n_seq, n_q_heads / n_kv_heads, n_kv_heads, head_dim, max_kv, device_sms(), &n_splits,
-                            &split_len);
-  return attn_scratch(n_tok, n_q_heads, head_dim, n_splits);
+  pcd::PagedPlan p;
+  pcd::plan_paged_attention(n_tok, n_seq, n_q_heads / n_kv_heads, n_kv_heads, max_kv, device_sms(), &p);
+  return attn_scratch(n_tok, n_q_heads, head_dim, p.n_splits);
 }
 
 extern "C" int pcd_k_paged_attention(const pcd_kv_pages* cache, const void* q, void* out, float* lse, int dtype,
@@ -245,13 +244,13 @@ extern "C" int pcd_k_paged_attention(const pcd_kv_pages* cache, const void* q, v
   a.x_tok = q_tok, a.x_head = q_head, a.out_tok = out_tok, a.out_head = out_head;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.err = dev_err;
-  pcd::plan_paged_attention(n_tok, n_seq, a.G, a.c.Hkv, a.c.dim, max_kv, device_sms(), &a.n_splits, &a.split_len);
-  const int64_t need = attn_scratch(n_tok, n_q_heads, a.c.dim, a.n_splits);
+  pcd::plan_paged_attention(n_tok, n_seq, a.G, a.c.Hkv, max_kv, device_sms(), &a.plan);
+  const int64_t need = attn_scratch(n_tok, n_q_heads, a.c.dim, a.plan.n_splits);
   if (need > 0) {
     PCD_REFUSE(!scratch || !aligned(scratch, 16) || scratch_bytes < need, PCD_ERR_INVALID_ARG,
                "scratch is smaller than pcd_k_paged_attention_scratch_bytes, or unaligned");
     a.part_o = static_cast<float*>(scratch);
-    a.part_ml = reinterpret_cast<float2*>(a.part_o + static_cast<int64_t>(a.n_splits) * n_tok * n_q_heads * a.c.dim);
+    a.part_ml = reinterpret_cast<float2*>(a.part_o + static_cast<int64_t>(a.plan.n_splits) * n_tok * n_q_heads * a.c.dim);
   }
   return launched(pcd::launch_paged_attention(a, static_cast<cudaStream_t>(stream)));
 }

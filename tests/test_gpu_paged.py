@@ -402,6 +402,14 @@ def test_attention_nan_stays_where_it_is_seen(paged, q_len):
     got = paged.pcd_k_paged_attention(*a)
     first_row = max(0, (L - 1) // 16 * 16 - (L - q_len))
     assert torch.equal(got[:first_row], clean[:first_row]) and torch.isnan(got[first_row:q_len, :2]).all()
+    assert torch.equal(got[:, 2:], clean[:, 2:])
+    ks[last, 0] = 1.0
+    vs[last, 1] = float("inf")
+    got = paged.pcd_k_paged_attention(*a)
+    assert torch.equal(got[:first_row], clean[:first_row]) and torch.isnan(got[first_row:q_len, 2:]).all()
+    vs[last, 1] = float("nan")
+    got = paged.pcd_k_paged_attention(*a)
+    assert torch.equal(got[:first_row], clean[:first_row]) and torch.isnan(got[first_row:q_len, 2:]).all()
 
 
 @pytest.mark.parametrize("q_len", [1, 50])
