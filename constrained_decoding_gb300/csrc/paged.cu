@@ -197,6 +197,10 @@ namespace {
 // order), and a V fragment's column is any channel, so a lane reads 16
 // consecutive channels of its four keys and pairs keys by byte permutes: no
 // ldmatrix, no transposition in shared memory.
+//
+// The ranges of a tile's keys are walked by a thread-block cluster that joins
+// them through distributed shared memory (up to 8 of them), or by CTAs that
+// leave their states to a second kernel.
 constexpr float kSlack = 7.f;
 constexpr int kWarps = 4, kStagesR = 4;
 
@@ -205,7 +209,8 @@ struct RowsCfg {
   static constexpr int kStage = 16 * D * 2;                       // 16 keys: K then V
   static constexpr int kRing = kWarps * kStagesR * kStage;
   static constexpr int kRedLd = D + 4;
-  static constexpr int kRed = kWarps * 16 * (kRedLd * 4 + 8);     // partial rows after the key loop
+  static constexpr int kRedMl = kWarps * 16 * kRedLd * 4;         // partial rows after the key loop, then (M, l)
+  static constexpr int kRed = kRedMl + (kWarps + 1) * 16 * 8;     // ... of the warps and of the CTA
   static constexpr int kSmem = kRing > kRed ? kRing : kRed;
 };
 
@@ -218,6 +223,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) paged_attn_rows_kernel(PagedAt
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
   const int hk = blockIdx.y, z = blockIdx.z;
+  // (what returns here returns in every CTA of a cluster)
   const SeqItem it = find_item(a.q, static_cast<int>(blockIdx.x), a.G, 4, 1);
   if (it.seq < 0) return;
   const int n = it.n;
@@ -235,65 +241,20 @@ __global__ void __launch_bounds__(kWarps * 32, 3) paged_attn_rows_kernel(PagedAt
   if (it.local >= (R + 15) >> 4) return;
   const int r0 = it.local * 16;
   const int r_end = min(r0 + 16, R);
+  const bool upper = r_end - r0 > 8;  // rows 8 .. 15 exist
   // keys seen by a row: all, or up to its own position
   const int first = a.causal ? len - n + 1 : len;  // by the sequence's first token
   auto seen = [&](int r) { return a.causal ? first + min(r, R - 1) / a.G : len; };
   const int kmax = max(0, seen(r_end - 1));
   const int kmin = max(0, seen(r0));
-  const int b0 = z * (a.plan.split_len >> 4);
-  const int b1 = z + 1 < a.plan.n_splits ? min((kmax + 15) >> 4, b0 + (a.plan.split_len >> 4)) : (kmax + 15) >> 4;
+  // this item's blocks in even ranges, whole rounds of the warps
+  const int bl = (kmax + 15) >> 4;
+  const int per = ((bl + a.plan.n_splits - 1) / a.plan.n_splits + kWarps - 1) / kWarps * kWarps;
+  const int b0 = min(bl, z * per), b1 = min(bl, b0 + per);
   const int nb = b1 > b0 + warp ? (b1 - b0 - warp + kWarps - 1) / kWarps : 0;  // blocks of this warp
 
-  // ---- Q fragments: k-step t takes channels (64 * (t / 4) + 16 c + 4 (t % 4)) + {0, 1 | 2, 3}
-  uint32_t qf[D / 16][4];
-  float qs[2];
-  float row_m[2] = {-INFINITY, -INFINITY}, row_l[2] = {0.f, 0.f};
-  int vis[2];
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const int r = r0 + g + 8 * e;
-    vis[e] = seen(r);
-    const bool ok = r < R;
-    const int tok = it.row0 + (ok ? r : r0) / a.G, hq = hk * a.G + (ok ? r : r0) % a.G;
-    const T* src = static_cast<const T*>(a.x) + tok * a.x_tok + hq * a.x_head;
-    float v[D / 16][4];
-    uint32_t am = 0;
-#pragma unroll
-    for (int t = 0; t < D / 16; ++t) {
-      const int d = 64 * (t >> 2) + 16 * c + 4 * (t & 3);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[t][i] = ok ? to_f(src[d + i]) : 0.f;
-        am = max(am, __float_as_uint(v[t][i]) & 0x7fffffffu);
-      }
-    }
-    am = max(am, __shfl_xor_sync(0xffffffffu, am, 1));
-    am = max(am, __shfl_xor_sync(0xffffffffu, am, 2));
-    float down;
-    qs[e] = row_power<T>(am, &down);
-#pragma unroll
-    for (int t = 0; t < D / 16; ++t) {
-      qf[t][e] = pack2(v[t][0] * down, v[t][1] * down);
-      qf[t][2 + e] = pack2(v[t][2] * down, v[t][3] * down);
-    }
-    qs[e] *= a.scale_log2 * (FMT == PCD_KV_E4M3 ? 256.f : 1.f);  // fp8_half: codes read as 2^-8 of themselves
-  }
-
-  float o[D / 8][4];
-#pragma unroll
-  for (int t = 0; t < D / 8; ++t)
-#pragma unroll
-    for (int i = 0; i < 4; ++i) o[t][i] = 0.f;
-
-  uint8_t* ring = smem + warp * (kStagesR * C::kStage);
+  // ---- page ids and constants of 32 of this warp's blocks at a time, one to a lane
   const int32_t* tab = a.q.table + static_cast<int64_t>(it.seq) * a.q.table_stride;
-  const uint8_t* kbase = a.c.k + hk * a.c.head_stride;
-  const uint8_t* vbase = a.c.v + hk * a.c.head_stride;
-  // page ids of 32 of this warp's blocks at a time, one to a lane
-  int ids = -1;
-  float sk = 0.f, sv = 0.f;
-  int ids_base = -32;
-  int nids = -1;  // the next 32
   auto block_at = [&](int i) { return b0 + warp + i * kWarps; };
   auto fetch_ids = [&](int i0) {
     const int i = i0 + lane;
@@ -307,102 +268,167 @@ __global__ void __launch_bounds__(kWarps * 32, 3) paged_attn_rows_kernel(PagedAt
     }
     return id;
   };
-  nids = fetch_ids(0);
+  int ids = fetch_ids(0), ids_next = fetch_ids(32);
+  float sk, lsv, isv;  // K scale, log2 and reciprocal of the V scale; isv 0: a page the table has wrong
+  auto scales = [&](int id) {
+    float k = 0.f, v = 1.f;
+    if (id >= 0) {
+      k = a.c.ks[static_cast<int64_t>(id) * a.c.Hkv + hk];
+      v = a.c.vs[static_cast<int64_t>(id) * a.c.Hkv + hk];
+      if (v < kScaleFloor) v = kScaleFloor;  // a NaN stays
+    }
+    sk = k;
+    lsv = lg2(v);
+    isv = id < 0 ? 0.f : 1.f / (v + (v - v));  // not finite: NaN
+  };
+
+  // ---- the ring: a lane copies the same 16 bytes of kCh / 2 keys of K and of V in every block
+  constexpr int kCh = D / 16;
+  uint8_t* ring = smem + warp * (kStagesR * C::kStage);
+  const int key0 = lane / kCh, ch = lane % kCh;  // and keys key0 + 32 / kCh, ...
+  const int step = static_cast<int>(a.c.tok_stride) * (32 / kCh);
+  const uint8_t* ksrc = a.c.k + hk * a.c.head_stride + key0 * a.c.tok_stride + ch * 16;
+  const int64_t vdelta = a.c.v - a.c.k;
+  uint32_t kdst = smem_u32(ring) + key0 * D + ((ch ^ ((key0 & 1) << 2)) & (kCh - 1)) * 16;
+  int ids_at = 0;  // `ids` holds blocks ids_at ..
   auto issue = [&](int i) {
     if (i < nb) {
-      if (i - ids_base >= 32) {  // the loads run ahead of the arithmetic by less than 32 blocks
-        ids = nids;
-        ids_base = i;
-        nids = fetch_ids(i + 32);
+      if (i - ids_at >= 32) {
+        ids = ids_next;
+        ids_at = i;
+        ids_next = fetch_ids(i + 32);
       }
-      const int id = __shfl_sync(0xffffffffu, ids, i - ids_base);
-      const int slot = (block_at(i) << 4) & ((1 << a.c.page_log2) - 1);
-      uint8_t* st = ring + (i % kStagesR) * C::kStage;
-      const int64_t off = (id < 0 ? 0 : id) * a.c.page_stride + slot * a.c.tok_stride;
-      constexpr int kCh = D / 16;
+      const int id = __shfl_sync(0xffffffffu, ids, i - ids_at);
+      const int j0 = block_at(i) << 4;
+      const int slot = j0 & ((1 << a.c.page_log2) - 1);
+      const uint8_t* src = ksrc + max(id, 0) * a.c.page_stride + slot * a.c.tok_stride;
+      const uint32_t st = (i % kStagesR) * C::kStage;
 #pragma unroll
       for (int e = 0; e < kCh / 2; ++e) {
-        const int x = e * 32 + lane, key = x / kCh, ch = x % kCh;
-        cp_async16(st + key * D + ((ch ^ ((key & 1) << 2)) & (kCh - 1)) * 16, kbase + off + key * a.c.tok_stride + ch * 16, id >= 0);
-        cp_async16(st + 16 * D + key * D + ((ch ^ (((key >> 1) & 3) << 1)) & (kCh - 1)) * 16, vbase + off + key * a.c.tok_stride + ch * 16, id >= 0);
+        const int key = key0 + e * (32 / kCh);
+        // slots behind the last token read as zeros, whatever they hold
+        const int bytes = id >= 0 && j0 + key < len ? 16 : 0;
+        cp_async16_to(kdst + st + e * (32 / kCh) * D, src + e * step, bytes);
+        cp_async16_to(smem_u32(ring) + st + 16 * D + key * D + ((ch ^ (((key >> 1) & 3) << 1)) & (kCh - 1)) * 16,
+                      src + vdelta + e * step, bytes);
       }
     }
     cp_async_commit();
   };
-  // scales of 32 blocks at a time
-  int cur_base = -32;
-  auto scales = [&](int i) {
-    if (i - cur_base >= 32) {
-      cur_base = i;
-      const int id = fetch_ids(i);
-      sk = id >= 0 ? a.c.ks[static_cast<int64_t>(id) * a.c.Hkv + hk] : 0.f;
-      sv = id >= 0 ? a.c.vs[static_cast<int64_t>(id) * a.c.Hkv + hk] : -1.f;
-      if (id >= 0 && sv < kScaleFloor) sv = kScaleFloor;  // a NaN stays
-    }
-  };
-
 #pragma unroll 1
   for (int i = 0; i < kStagesR - 1; ++i) issue(i);
+  scales(ids);
+  int sc_at = 0;
+
+  // ---- Q fragments: k-step t takes channels (64 * (t / 4) + 16 c + 4 (t % 4)) + {0, 1 | 2, 3}
+  uint32_t qf[D / 16][4];
+  float qs[2];
+  float row_m[2] = {-INFINITY, -INFINITY}, row_l[2] = {0.f, 0.f};
+  int vis[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int r = r0 + g + 8 * e;
+    vis[e] = seen(r);
+    const bool ok = r < R;
+    const int tok = it.row0 + (ok ? r : r0) / a.G, hq = hk * a.G + (ok ? r : r0) % a.G;
+    const T* src = static_cast<const T*>(a.x) + tok * a.x_tok + hq * a.x_head;
+    const bool wide = (reinterpret_cast<uintptr_t>(src) & 7) == 0;
+    alignas(8) T v[D / 16][4];
+    uint32_t am = 0;
+#pragma unroll
+    for (int t = 0; t < D / 16; ++t) {
+      const int d = 64 * (t >> 2) + 16 * c + 4 * (t & 3);
+      if (!ok) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[t][i] = from_f<T>(0.f);
+      } else if (wide) {
+        *reinterpret_cast<uint2*>(v[t]) = *reinterpret_cast<const uint2*>(src + d);
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[t][i] = src[d + i];
+      }
+    }
+    if (!std::is_same<T, __half>::value) {
+#pragma unroll
+      for (int t = 0; t < D / 16; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) am = max(am, __float_as_uint(to_f(v[t][i])) & 0x7fffffffu);
+      am = max(am, __shfl_xor_sync(0xffffffffu, am, 1));
+      am = max(am, __shfl_xor_sync(0xffffffffu, am, 2));
+    }
+    float down;
+    qs[e] = row_power<T>(am, &down) * a.scale_log2;
+#pragma unroll
+    for (int t = 0; t < D / 16; ++t) {
+      qf[t][e] = pack2(to_f(v[t][0]) * down, to_f(v[t][1]) * down);
+      qf[t][2 + e] = pack2(to_f(v[t][2]) * down, to_f(v[t][3]) * down);
+    }
+  }
+
+  float o[D / 8][4];
+#pragma unroll
+  for (int t = 0; t < D / 8; ++t)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[t][i] = 0.f;
+
 #pragma unroll 1
   for (int i = 0; i < nb; ++i) {
     cp_async_wait<kStagesR - 2>();
     __syncwarp();
+    if (i - sc_at >= 32) {
+      sc_at = i;
+      scales(fetch_ids(i));
+    }
     issue(i + kStagesR - 1);
-    scales(i);
-    const float bsk = __shfl_sync(0xffffffffu, sk, i - cur_base);
-    const float bsv = __shfl_sync(0xffffffffu, sv, i - cur_base);
+    const float bsk = __shfl_sync(0xffffffffu, sk, i - sc_at);
+    const float blsv = __shfl_sync(0xffffffffu, lsv, i - sc_at);
+    const float bisv = __shfl_sync(0xffffffffu, isv, i - sc_at);
     const uint8_t* st = ring + (i % kStagesR) * C::kStage;
     // ---- S = Q K^T: two tiles of 8 keys
     float s[2][4];
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
-      const int key = 8 * t + g;
+    for (int t = 0; t < 2; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
 #pragma unroll
-      for (int hf = 0; hf < D / 64; ++hf) {
-        const int ch = c + 4 * hf;
-        const uint4 w = *reinterpret_cast<const uint4*>(st + key * D + ((ch ^ ((key & 1) << 2)) & (D / 16 - 1)) * 16);
-        const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+    for (int hf = 0; hf < D / 64; ++hf) {
+      uint4 w[2];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+      for (int t = 0; t < 2; ++t) {
+        const int key = 8 * t + g;
+        w[t] = *reinterpret_cast<const uint4*>(st + key * D + (((c + 4 * hf) ^ ((key & 1) << 2)) & (kCh - 1)) * 16);
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
           uint32_t h0, h1;
-          codes4_half<FMT>(ww[q], &h0, &h1);
+          codes4_half<FMT>(q == 0 ? w[t].x : q == 1 ? w[t].y : q == 2 ? w[t].z : w[t].w, &h0, &h1);
           mma16816(s[t], qf[4 * hf + q], h0, h1);
         }
-      }
     }
-    // ---- weights
+    // ---- weights (rows 8 .. 15 only where the tile has them)
     const int j0 = block_at(i) << 4;
-    const float lsv = lg2(bsv);
-    const bool bad = bsv == -1.f;  // a page the table has wrong: nothing of it is seen
-    // a poisoned scale (NaN) counts only for rows that see its keys
-    const float iv[2] = {bad || vis[0] <= j0 ? 0.f : 1.f / bsv, bad || vis[1] <= j0 ? 0.f : 1.f / bsv};
-    float ak[2];
-    ak[0] = qs[0] * bsk;
-    ak[1] = qs[1] * bsk;
-    if (j0 + 16 > kmin || bad) {
+    uint32_t pf[4];
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+    for (int e = 0; e < 2; ++e) {
+      if (e == 1 && !upper) {
+        pf[1] = pf[3] = 0u;
+        break;
+      }
+      const float ak = qs[e] * bsk;
+      float x[4] = {s[0][2 * e], s[0][2 * e + 1], s[1][2 * e], s[1][2 * e + 1]};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int j = j0 + 8 * t + 2 * c + (e & 1);
-          const float x = fmaf(s[t][e], ak[e >> 1], lsv);
-          s[t][e] = (j < vis[e >> 1] && !bad) ? x : -INFINITY;
-        }
-    } else {
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[t][e] = fmaf(s[t][e], ak[e >> 1], lsv);
-    }
-    float mx[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e)
-      mx[e] = fmaxf(fmaxf(s[0][2 * e], s[0][2 * e + 1]), fmaxf(s[1][2 * e], s[1][2 * e + 1]));
-    if (__any_sync(0xffffffffu, mx[0] > row_m[0] + kSlack || mx[1] > row_m[1] + kSlack)) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float m = mx[e];
+      for (int k = 0; k < 4; ++k) x[k] = fmaf(x[k], ak, blsv);
+      float iv = bisv;
+      if (j0 + 16 > kmin || bisv == 0.f) {
+        const int lim = bisv == 0.f ? 0 : vis[e] - j0 - 2 * c;
+        x[0] = 0 < lim ? x[0] : -INFINITY;
+        x[1] = 1 < lim ? x[1] : -INFINITY;
+        x[2] = 8 < lim ? x[2] : -INFINITY;
+        x[3] = 9 < lim ? x[3] : -INFINITY;
+        if (vis[e] <= j0) iv = 0.f;  // a poisoned scale (NaN) counts only for rows that see its keys
+      }
+      float m = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+      if (__any_sync(0xffffffffu, m > row_m[e] + kSlack)) {
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
         m = fmaxf(m, row_m[e]);
@@ -415,28 +441,22 @@ __global__ void __launch_bounds__(kWarps * 32, 3) paged_attn_rows_kernel(PagedAt
           o[t][2 * e + 1] *= f;
         }
       }
+      const float mb = (row_m[e] == -INFINITY ? 0.f : row_m[e]) - kBias;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) x[k] = ex2_approx(x[k] - mb);
+      row_l[e] = fmaf((x[0] + x[1]) + (x[2] + x[3]), iv, row_l[e]);
+      pf[e] = pack2(x[0], x[1]);
+      pf[2 + e] = pack2(x[2], x[3]);
     }
-    float mb[2];
-#pragma unroll
-    for (int e = 0; e < 2; ++e) mb[e] = (row_m[e] == -INFINITY ? 0.f : row_m[e]) - kBias;
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        s[t][e] = ex2_approx(s[t][e] - mb[e >> 1]);
-        row_l[e >> 1] = fmaf(s[t][e], iv[e >> 1], row_l[e >> 1]);
-      }
-    const uint32_t pf[4] = {pack2(s[0][0], s[0][1]), pack2(s[0][2], s[0][3]), pack2(s[1][0], s[1][1]),
-                            pack2(s[1][2], s[1][3])};
-    // ---- O += P V: column tile t's lane group g is channel g * (D / 8) + t
-    const uint8_t* sv_ = st + 16 * D;
+    // ---- O += w V: column tile t's lane group g is channel g * (D / 8) + t
+    const uint8_t* sv = st + 16 * D;
     constexpr int kLd = D / 8;  // channels of a lane: 16 or 8 bytes
     uint32_t vr[4][kLd / 4];
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk) {
       const int key = 2 * c + (kk & 1) + 8 * (kk >> 1);
-      const int byte = g * kLd, ch = byte >> 4;
-      const uint8_t* p = sv_ + key * D + ((ch ^ (((key >> 1) & 3) << 1)) & (D / 16 - 1)) * 16 + (byte & 15);
+      const int byte = g * kLd;
+      const uint8_t* p = sv + key * D + (((byte >> 4) ^ (((key >> 1) & 3) << 1)) & (kCh - 1)) * 16 + (byte & 15);
       if constexpr (kLd == 16) {
         const uint4 w = *reinterpret_cast<const uint4*>(p);
         vr[kk][0] = w.x, vr[kk][1] = w.y, vr[kk][2] = w.z, vr[kk][3] = w.w;
@@ -446,10 +466,12 @@ __global__ void __launch_bounds__(kWarps * 32, 3) paged_attn_rows_kernel(PagedAt
       }
     }
 #pragma unroll
-    for (int t = 0; t < D / 8; ++t) {
-      const uint32_t v0 = codes_pair_half<FMT>(vr[0][t >> 2], vr[1][t >> 2], t & 3);
-      const uint32_t v1 = codes_pair_half<FMT>(vr[2][t >> 2], vr[3][t >> 2], t & 3);
-      mma16816(o[t], pf, v0, v1);
+    for (int t = 0; t < D / 8; t += 2) {
+      uint32_t v0[2], v1[2];
+      codes_cross_half<FMT>(vr[0][t >> 2], vr[1][t >> 2], (t >> 1) & 1, &v0[0], &v0[1]);
+      codes_cross_half<FMT>(vr[2][t >> 2], vr[3][t >> 2], (t >> 1) & 1, &v1[0], &v1[1]);
+      mma16816(o[t], pf, v0[0], v1[0]);
+      mma16816(o[t + 1], pf, v0[1], v1[1]);
     }
     __syncwarp();
   }
@@ -462,7 +484,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) paged_attn_rows_kernel(PagedAt
   // ---- join the warps
   __syncthreads();
   float* red = reinterpret_cast<float*>(smem);
-  float2* ml = reinterpret_cast<float2*>(smem + kWarps * 16 * C::kRedLd * 4);
+  float2* ml = reinterpret_cast<float2*>(smem + C::kRedMl);
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     const int r = g + 8 * e;
@@ -470,11 +492,12 @@ __global__ void __launch_bounds__(kWarps * 32, 3) paged_attn_rows_kernel(PagedAt
 #pragma unroll
     for (int t = 0; t < D / 8; ++t)  // accumulator column 2c + i is lane group 2c + i's channel
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        red[(warp * 16 + r) * C::kRedLd + (2 * c + i) * (D / 8) + t] = o[t][2 * e + i];
+      for (int i = 0; i < 2; ++i) red[(warp * 16 + r) * C::kRedLd + (2 * c + i) * (D / 8) + t] = o[t][2 * e + i];
   }
   __syncthreads();
-  for (int x = threadIdx.x; x < (r_end - r0) * (D / 4); x += kWarps * 32) {
+  const bool cluster = a.plan.cluster != 0;
+  const int work = (r_end - r0) * (D / 4);
+  for (int x = threadIdx.x; x < work; x += kWarps * 32) {
     const int r = x / (D / 4), d = (x % (D / 4)) * 4;
     RowState st;
 #pragma unroll
@@ -482,14 +505,36 @@ __global__ void __launch_bounds__(kWarps * 32, 3) paged_attn_rows_kernel(PagedAt
 #pragma unroll
     for (int w = 0; w < kWarps; ++w)
       st.add(ml[w * 16 + r], *reinterpret_cast<const float4*>(red + (w * 16 + r) * C::kRedLd + d));
-    const int rr = r0 + r, tok = it.row0 + rr / a.G, hq = hk * a.G + rr % a.G;
-    finish_row<T>(a, st, z, tok, hq, d, FMT == PCD_KV_E4M3 ? 256.f : 1.f);
+    if (cluster) {  // warp 0's rows now hold the CTA's: each thread read what it overwrites
+      *reinterpret_cast<float4*>(red + r * C::kRedLd + d) = st.o;
+      if (d == 0) ml[kWarps * 16 + r] = make_float2(st.M, st.L);
+    } else {
+      const int rr = r0 + r;
+      finish_row<T>(a, st, a.plan.n_splits > 1, z, it.row0 + rr / a.G, hk * a.G + rr % a.G, d);
+    }
   }
+  if (!cluster) return;
+  cluster_sync_all();
+  const int nz = a.plan.n_splits;
+  for (int x = z * kWarps * 32 + threadIdx.x; x < work; x += nz * kWarps * 32) {
+    const int r = x / (D / 4), d = (x % (D / 4)) * 4;
+    RowState st;
+    float2 m[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (q < nz) st.top(m[q] = dsmem_ld_f2(dsmem_addr(ml + kWarps * 16 + r, q)));
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (q < nz) st.add(m[q], dsmem_ld_f4(dsmem_addr(red + r * C::kRedLd + d, q)));
+    const int rr = r0 + r;
+    finish_row<T>(a, st, false, 0, it.row0 + rr / a.G, hk * a.G + rr % a.G, d);
+  }
+  cluster_sync_all();  // no CTA leaves while another reads its shared memory
 }
 
 // Joins the key ranges of a row: out = sum 2^(M_i - M) O_i / sum 2^(M_i - M) l_i.
 template <int D, class T>
-__global__ void __launch_bounds__(256) paged_attn_join_kernel(PagedAttnArgs a, float unit) {
+__global__ void __launch_bounds__(256) paged_attn_join_kernel(PagedAttnArgs a) {
   griddep_launch_dependents();
   griddep_wait();
   constexpr int kPer = D / 4;  // threads of a row
@@ -506,20 +551,38 @@ __global__ void __launch_bounds__(256) paged_attn_join_kernel(PagedAttnArgs a, f
     if (ml.y == 0.f) continue;
     st.add(ml, *reinterpret_cast<const float4*>(a.part_o + (z * rows + row) * D + d));
   }
-  PagedAttnArgs b = a;
-  b.plan.n_splits = 1;
-  finish_row<T>(b, st, 0, tok, hq, d, unit);
+  finish_row<T>(a, st, false, 0, tok, hq, d);
 }
 
 template <int D, int FMT, class T>
 int launch_rows(const PagedAttnArgs& a, cudaStream_t s) {
   using C = RowsCfg<D>;
   auto kern = paged_attn_rows_kernel<D, FMT, T>;
-  cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  const cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
   if (r != cudaSuccess) return r;
-  const int64_t items = ((static_cast<int64_t>(a.q.n_tok) * a.G) >> 4) + a.q.n_seq;
-  return launch_k(kern, dim3(static_cast<unsigned>(items), static_cast<unsigned>(a.c.Hkv), static_cast<unsigned>(a.plan.n_splits)),
-                  dim3(kWarps * 32), C::kSmem, s, a);
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(((static_cast<int64_t>(a.q.n_tok) * a.G) >> 4) + a.q.n_seq),
+                     static_cast<unsigned>(a.c.Hkv), static_cast<unsigned>(a.plan.n_splits));
+  cfg.blockDim = dim3(kWarps * 32);
+  cfg.dynamicSmemBytes = C::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  int na = 0;
+  if (a.plan.cluster) {
+    at[na].id = cudaLaunchAttributeClusterDimension;
+    at[na].val.clusterDim.x = 1;
+    at[na].val.clusterDim.y = 1;
+    at[na].val.clusterDim.z = static_cast<unsigned>(a.plan.n_splits);
+    ++na;
+  }
+  if (pdl_enabled()) {
+    at[na].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[na].val.programmaticStreamSerializationAllowed = 1;
+    ++na;
+  }
+  cfg.attrs = at;
+  cfg.numAttrs = na;
+  return cudaLaunchKernelEx(&cfg, kern, a);
 }
 
 template <int D, int FMT>
@@ -533,13 +596,15 @@ void plan_paged_attention(int n_tok, int n_seq, int G, int Hkv, int64_t max_kv, 
   const int64_t per = n_seq > 0 ? (n_tok + n_seq - 1) / n_seq : 0;  // query tokens of a sequence, on average
   p->rows = per * G > 32 ? 256 : 16;
   const int64_t tiles = std::max<int64_t>(1, n_seq * ((per * G + p->rows - 1) / p->rows) * Hkv);
-  const int64_t unit = p->rows == 16 ? 64 : 128;  // keys that a range is a multiple of
-  int64_t want = p->rows == 16 ? (static_cast<int64_t>(sms) * 12 + tiles - 1) / tiles : sms / tiles;
-  want = std::min<int64_t>(std::max<int64_t>(want, 1), 256);
-  int64_t len = (max_kv + want - 1) / want;
-  len = std::max<int64_t>(unit, (len + unit - 1) / unit * unit);
-  p->split_len = static_cast<int>(std::min<int64_t>(len, 1 << 30));
-  p->n_splits = static_cast<int>(std::max<int64_t>(1, (max_kv + len - 1) / len));
+  int64_t want;
+  if (p->rows == 16) {
+    want = std::min((static_cast<int64_t>(sms) * 12 + tiles - 1) / tiles, (max_kv + 63) / 64);
+    p->cluster = want > 1 && want <= 8;
+  } else {
+    want = std::min<int64_t>(sms / tiles, (max_kv + 127) / 128);
+    p->cluster = 0;
+  }
+  p->n_splits = static_cast<int>(std::min<int64_t>(std::max<int64_t>(want, 1), 256));
 }
 
 int launch_paged_attention(const PagedAttnArgs& a, cudaStream_t s) {
@@ -552,16 +617,15 @@ int launch_paged_attention(const PagedAttnArgs& a, cudaStream_t s) {
     r = f8 ? launch_rows_t<64, PCD_KV_E4M3>(a, s) : launch_rows_t<64, PCD_KV_INT8>(a, s);
   else
     r = f8 ? launch_rows_t<128, PCD_KV_E4M3>(a, s) : launch_rows_t<128, PCD_KV_INT8>(a, s);
-  if (r != 0 || a.plan.n_splits == 1) return r;
-  const float unit = f8 ? 256.f : 1.f;
+  if (r != 0 || a.plan.n_splits == 1 || a.plan.cluster) return r;
   const int64_t threads = static_cast<int64_t>(a.q.n_tok) * a.Hq * (a.c.dim / 4);
   const dim3 grid(static_cast<unsigned>((threads + 255) / 256));
   const bool bf = a.dtype == PCD_DTYPE_BF16;
   if (a.c.dim == 64)
-    return bf ? launch_k(paged_attn_join_kernel<64, __nv_bfloat16>, grid, dim3(256), 0, s, a, unit)
-              : launch_k(paged_attn_join_kernel<64, __half>, grid, dim3(256), 0, s, a, unit);
-  return bf ? launch_k(paged_attn_join_kernel<128, __nv_bfloat16>, grid, dim3(256), 0, s, a, unit)
-            : launch_k(paged_attn_join_kernel<128, __half>, grid, dim3(256), 0, s, a, unit);
+    return bf ? launch_k(paged_attn_join_kernel<64, __nv_bfloat16>, grid, dim3(256), 0, s, a)
+              : launch_k(paged_attn_join_kernel<64, __half>, grid, dim3(256), 0, s, a);
+  return bf ? launch_k(paged_attn_join_kernel<128, __nv_bfloat16>, grid, dim3(256), 0, s, a)
+            : launch_k(paged_attn_join_kernel<128, __half>, grid, dim3(256), 0, s, a);
 }
 
 }  // namespace pcd

@@ -83,6 +83,7 @@ __device__ __forceinline__ float block_scale(float am, float old, bool held, int
   return need;
 }
 __device__ __forceinline__ uint8_t encode(float x, int format) {
+  if (x != x) return 0;  // the scale says so: no code is a NaN
   if (format == PCD_KV_INT8) return static_cast<uint8_t>(static_cast<int8_t>(max(-127, min(127, __float2int_rn(x)))));
   return __nv_cvt_float_to_fp8(x, __NV_SATFINITE, __NV_E4M3);
 }
@@ -91,37 +92,34 @@ __device__ __forceinline__ float decode(uint8_t q, int format) {
   return __half2float(__half(__nv_cvt_fp8_to_halfraw(q, __NV_E4M3)));
 }
 
-// Two codes in the upper bytes of a register's halves as fp16.  e4m3 shares
-// fp16's layout shifted by one bit, with a bias of 7 for 15: the halves hold
-// 2^-8 of the values, subnormals included.  (0x7f, its NaN, reads as 480: a
-// NaN shows in the block's scale instead.)
-__device__ __forceinline__ uint32_t fp8_half(uint32_t x) { return (x & 0x80008000u) | ((x >> 1) & 0x3f803f80u); }
-// int8 codes with the sign bit flipped, under the exponent of 1024.
+// Codes as fp16, exactly.  e4m3 by the conversion instruction (64 lanes a
+// clock on an SM, four times what masks and shifts reach); int8 with the sign
+// bit flipped as the low mantissa bits of 1024, minus 1152.
+__device__ __forceinline__ uint32_t e4m3x2_half(uint32_t two) {
+  uint32_t h;
+  asm("{\n\t.reg .b16 lo;\n\tcvt.u16.u32 lo, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(h) : "r"(two));
+  return h;
+}
 __device__ __forceinline__ uint32_t int8_half(uint32_t x) {
-  const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&x), __half2half2(__ushort_as_half(0x6480)));  // - 1152
+  const __half2 h = __hsub2(*reinterpret_cast<const __half2*>(&x), __half2half2(__ushort_as_half(0x6480)));
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 // Codes 0, 1 and 2, 3 of a word.
 template <int FMT>
 __device__ __forceinline__ void codes4_half(uint32_t w, uint32_t* h0, uint32_t* h1) {
   if constexpr (FMT == PCD_KV_E4M3) {
-    *h0 = fp8_half(__byte_perm(w, 0, 0x1404));
-    *h1 = fp8_half(__byte_perm(w, 0, 0x3424));
+    *h0 = e4m3x2_half(w);
+    *h1 = e4m3x2_half(w >> 16);
   } else {
     w ^= 0x80808080u;
     *h0 = int8_half(__byte_perm(w, 0x64646464u, 0x4140));
     *h1 = int8_half(__byte_perm(w, 0x64646464u, 0x4342));
   }
 }
-// Code b of two words.
+// Codes 2b, 2b + 1 of two words, paired across the words.
 template <int FMT>
-__device__ __forceinline__ uint32_t codes_pair_half(uint32_t w0, uint32_t w1, int b) {
-  if constexpr (FMT == PCD_KV_E4M3) {
-    return fp8_half(__byte_perm(w0, w1, (b << 4) | ((4 + b) << 12)));  // the lower bytes fall to fp8_half's masks
-  } else {
-    const uint32_t p = __byte_perm(w0, w1, b | ((4 + b) << 8));
-    return int8_half(((p ^ 0x00800080u) & 0x00ff00ffu) | 0x64006400u);
-  }
+__device__ __forceinline__ void codes_cross_half(uint32_t w0, uint32_t w1, int b, uint32_t* h0, uint32_t* h1) {
+  codes4_half<FMT>(__byte_perm(w0, w1, b ? 0x7362 : 0x5140), h0, h1);
 }
 
 // ----------------------------------------------------------------------- rows
@@ -166,15 +164,15 @@ struct RowState {
 };
 // Writes 4 channels of a row: the output, or the partial of key range z.
 template <class T>
-__device__ __forceinline__ void finish_row(const PagedAttnArgs& a, const RowState& st, int z, int tok, int hq, int d,
-                                           float unit) {
-  if (a.plan.n_splits > 1) {
+__device__ __forceinline__ void finish_row(const PagedAttnArgs& a, const RowState& st, bool partial, int z, int tok, int hq,
+                                           int d) {
+  if (partial) {
     const int64_t row = (static_cast<int64_t>(z) * a.q.n_tok + tok) * a.Hq + hq;
     if (d == 0) a.part_ml[row] = make_float2(st.M, st.L);
     if (st.L != 0.f) *reinterpret_cast<float4*>(a.part_o + row * a.c.dim + d) = st.o;
     return;
   }
-  const float il = st.L == 0.f ? 0.f : unit / st.L;
+  const float il = st.L == 0.f ? 0.f : 1.f / st.L;
   T* out = static_cast<T*>(a.out) + tok * a.out_tok + hq * a.out_head + d;
   out[0] = from_f<T>(st.o.x * il);
   out[1] = from_f<T>(st.o.y * il);

@@ -59,9 +59,10 @@ struct AppendArgs {
 int launch_kv_append(const AppendArgs& a, cudaStream_t s);
 
 // How a call is cut up: query rows of a work item (16: warp MMA, 256:
-// tcgen05) and key ranges of split_len, the last taking the rest.
+// tcgen05) and the ranges that every item's keys are divided into; `cluster`:
+// a thread-block cluster walks the ranges of an item and joins them itself.
 struct PagedPlan {
-  int rows, n_splits, split_len;
+  int rows, n_splits, cluster;
 };
 
 struct PagedAttnArgs {
@@ -74,7 +75,7 @@ struct PagedAttnArgs {
   int64_t x_tok, x_head, out_tok, out_head;  // elements
   float scale_log2;                          // softmax scale x log2(e)
   PagedPlan plan;
-  float* part_o;                             // [n_splits][n_tok][Hq][dim], plan.n_splits > 1
+  float* part_o;                             // [n_splits][n_tok][Hq][dim], when ranges are joined by a second kernel
   float2* part_ml;                           // [n_splits][n_tok][Hq]
   int* err;
 };

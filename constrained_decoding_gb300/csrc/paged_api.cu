@@ -35,7 +35,7 @@ int device_sms() {
   int dev = 0, sms = 0;
   cudaGetDevice(&dev);
   cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  return sms > 0 ? sms : 1;
+  return sms > 0 ? sms : 152;  // no GPU here: a GB300's, so sizes can be asked for
 }
 
 int launched(int r) {
@@ -71,6 +71,7 @@ int view_pages(const pcd_kv_pages* c, pcd::PagesView* v) {
   PCD_REFUSE(!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4) ||
                  page % 16 || head % 16 || tok % 16,
              PCD_ERR_INVALID_ARG, "cache: rows of codes start at multiples of 16 bytes");
+  PCD_REFUSE(tok > (1 << 24), PCD_ERR_INVALID_ARG, "cache: token_stride is at most 2^24");
   PCD_REFUSE(tok < c->head_dim || (c->n_kv_heads > 1 && head < c->head_dim) || (c->n_pages > 1 && page < c->head_dim),
              PCD_ERR_INVALID_ARG, "cache: strides overlap rows");
   *v = pcd::PagesView{static_cast<uint8_t*>(c->k), static_cast<uint8_t*>(c->v), c->k_scale, c->v_scale, page, head, tok,
@@ -198,9 +199,9 @@ extern "C" int pcd_k_kv_append(const pcd_kv_pages* cache, const void* k, const v
 }
 
 namespace {
-int64_t attn_scratch(int n_tok, int Hq, int dim, int n_splits) {
-  if (n_splits <= 1) return 0;
-  return static_cast<int64_t>(n_splits) * n_tok * Hq * (dim * 4 + 8);
+int64_t attn_scratch(int n_tok, int Hq, int dim, const pcd::PagedPlan& p) {
+  if (p.n_splits <= 1 || p.cluster) return 0;
+  return static_cast<int64_t>(p.n_splits) * n_tok * Hq * (dim * 4 + 8);
 }
 }  // namespace
 
@@ -211,7 +212,7 @@ extern "C" int64_t pcd_k_paged_attention_scratch_bytes(int n_tok, int n_seq, int
     return 0;
   pcd::PagedPlan p;
   pcd::plan_paged_attention(n_tok, n_seq, n_q_heads / n_kv_heads, n_kv_heads, max_kv, device_sms(), &p);
-  return attn_scratch(n_tok, n_q_heads, head_dim, p.n_splits);
+  return attn_scratch(n_tok, n_q_heads, head_dim, p);
 }
 
 extern "C" int pcd_k_paged_attention(const pcd_kv_pages* cache, const void* q, void* out, float* lse, int dtype,
@@ -245,7 +246,7 @@ extern "C" int pcd_k_paged_attention(const pcd_kv_pages* cache, const void* q, v
   a.scale_log2 = scale * 1.4426950408889634f;
   a.err = dev_err;
   pcd::plan_paged_attention(n_tok, n_seq, a.G, a.c.Hkv, max_kv, device_sms(), &a.plan);
-  const int64_t need = attn_scratch(n_tok, n_q_heads, a.c.dim, a.plan.n_splits);
+  const int64_t need = attn_scratch(n_tok, n_q_heads, a.c.dim, a.plan);
   if (need > 0) {
     PCD_REFUSE(!scratch || !aligned(scratch, 16) || scratch_bytes < need, PCD_ERR_INVALID_ARG,
                "scratch is smaller than pcd_k_paged_attention_scratch_bytes, or unaligned");

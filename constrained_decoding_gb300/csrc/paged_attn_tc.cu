@@ -128,10 +128,10 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
   const int first = a.causal ? len - it.n + 1 : len;
   auto seen = [&](int r) { return max(0, a.causal ? first + r / a.G : len); };
   const int kmax = seen(r_end - 1);
-  const int b0 = z * (a.plan.split_len / kBlock);
   const int bl = (kmax + kBlock - 1) / kBlock;
-  const int b1 = z + 1 < a.plan.n_splits ? min(bl, b0 + a.plan.split_len / kBlock) : bl;
-  const int nb = max(0, b1 - b0);
+  const int per = (bl + a.plan.n_splits - 1) / a.plan.n_splits;  // this item's blocks, in even ranges
+  const int b0 = min(bl, z * per);
+  const int nb = min(bl, b0 + per) - b0;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
         where(j, &row, &ch);
         const int key = b * kBlock + row;
         const int pg = key >> a.c.page_log2;
-        const int id = pg <= last_page ? tab[pg] : -1;
+        const int id = key < len ? tab[pg] : -1;  // slots behind the last token read as zeros, whatever they hold
         v[j] = make_uint4(0u, 0u, 0u, 0u);
         if (id >= 0 && id < a.c.n_pages)
           v[j] = *reinterpret_cast<const uint4*>(base + id * a.c.page_stride + hk * a.c.head_stride +
@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
         }
       }
       float down;
-      qs = row_power<T>(am, &down) * a.scale_log2 * (FMT == PCD_KV_E4M3 ? 256.f : 1.f);
+      qs = row_power<T>(am, &down) * a.scale_log2;
       uint8_t* q = smem + t * C::kOp;
 #pragma unroll 4
       for (int c = 0; c < D / 8; ++c) {
@@ -443,7 +443,7 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
     const bool split = a.plan.n_splits > 1;
     const int64_t prow = (static_cast<int64_t>(z) * a.q.n_tok + tok) * a.Hq + hq;
     T* out = static_cast<T*>(a.out) + tok * a.out_tok + hq * a.out_head;
-    const float il = l == 0.f ? 0.f : (FMT == PCD_KV_E4M3 ? 256.f : 1.f) / l;
+    const float il = l == 0.f ? 0.f : 1.f / l;
     if (active) {
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {

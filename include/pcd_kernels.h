@@ -195,12 +195,12 @@ int pcd_k_rope(const void* x, void* y, int dtype, int n_tok, int heads, int head
 
 /* A pool of cache pages in 8 bits.  The K and V codes of (page, KV head, slot)
  * are head_dim bytes at page * page_stride + head * head_stride + slot *
- * token_stride of `k` and `v` (strides and bases multiples of 16 bytes), so
- * both [page][head][slot] and [page][slot][head] orders serve.  A page holds
+ * token_stride of `k` and `v` (strides and bases multiples of 16 bytes,
+ * token_stride at most 2^24), so both [page][head][slot] and [page][slot][head] orders serve.  A page holds
  * page_size (16, 32, 64 or 128) consecutive tokens of one sequence; each
  * (page, KV head) has one scale in k_scale / v_scale [n_pages][n_kv_heads],
  * fp32: value = code * scale.  head_dim 64 or 128. */
-#define PCD_KV_E4M3 1 /* 8-bit floats, 4 exponent bits; scales are powers of two when written here */
+#define PCD_KV_E4M3 1 /* 8-bit floats, 4 exponent bits; scales are powers of two when written here, and no code is NaN */
 #define PCD_KV_INT8 2 /* signed integers, -127 .. 127 */
 typedef struct {
   void *k, *v;

@@ -94,7 +94,7 @@ BAD_PAGES = [
     dict(k=None), dict(v=None), dict(k_scale=None), dict(v_scale=None), dict(k=BASE + 8), dict(v=BASE + 1), dict(k_scale=BASE + 2),
     dict(page_size=8), dict(page_size=48), dict(page_size=256), dict(page_size=0), dict(n_pages=0), dict(n_kv_heads=0),
     dict(n_kv_heads=70000), dict(format=0), dict(format=3), dict(page_stride=2056), dict(head_stride=1032), dict(token_stride=72),
-    dict(token_stride=48), dict(token_stride=0), dict(token_stride=-64), dict(head_stride=0), dict(page_stride=0),
+    dict(token_stride=48), dict(token_stride=0), dict(token_stride=-64), dict(token_stride=(1 << 24) + 16), dict(head_stride=0), dict(page_stride=0),
 ]
 
 
