@@ -198,9 +198,12 @@ namespace {
 // consecutive channels of its four keys and pairs keys by byte permutes: no
 // ldmatrix, no transposition in shared memory.
 //
-// The ranges of a tile's keys are walked by a thread-block cluster that joins
-// them through distributed shared memory (up to 8 of them), or by CTAs that
-// leave their states to a second kernel.
+// How the work is cut: small calls give every item (a tile of one KV head) to a
+// thread-block cluster of up to 8 CTAs that divide its keys and join through
+// distributed shared memory.  Large ones lay the 16-key blocks of all items on
+// one line and give each of the resident CTAs the same stretch of it, so
+// ragged lengths leave nobody idle; states of items that a stretch's end cuts go
+// to scratch, and a second kernel joins them.
 constexpr float kSlack = 7.f;
 constexpr int kWarps = 4, kStagesR = 4;
 
@@ -214,6 +217,34 @@ struct RowsCfg {
   static constexpr int kSmem = kRing > kRed ? kRing : kRed;
 };
 
+// A sequence as the rows kernel divides it.
+struct RowsSeq {
+  int row0, n, len, tiles, blocks;  // tiles of 16 rows (0: nothing to do), 16-key blocks of an item
+};
+__device__ __forceinline__ RowsSeq rows_seq(const PagedAttnArgs& a, int s) {
+  RowsSeq q;
+  q.row0 = a.q.q_off[s];
+  q.n = a.q.q_off[s + 1] - q.row0;
+  q.len = a.q.kv_len[s];
+  q.tiles = 0;
+  if (q.n != 0) {
+    if (q.n < 0 || q.row0 < 0 || q.n > a.q.n_tok - q.row0) {
+      record_error(a.err, DEV_BAD_INDEX);
+    } else {
+      q.tiles = (q.n * a.G + 15) >> 4;
+      if (q.len < 0 || q.len > kMaxLen || q.len > static_cast<int64_t>(a.q.table_stride) << a.c.page_log2) {
+        record_error(a.err, DEV_BAD_INDEX);
+        q.len = 0;
+      }
+    }
+  }
+  q.blocks = max(1, (q.len + 15) >> 4);  // an item without keys still writes its rows
+  return q;
+}
+__device__ __forceinline__ int64_t rows_units(const PagedAttnArgs& a, const RowsSeq& q) {
+  return static_cast<int64_t>(q.tiles) * a.c.Hkv * q.blocks;
+}
+
 template <int D, int FMT, class T>
 __global__ void __launch_bounds__(kWarps * 32, 3) paged_attn_rows_kernel(PagedAttnArgs a) {
   using C = RowsCfg<D>;
@@ -222,24 +253,69 @@ __global__ void __launch_bounds__(kWarps * 32, 3) paged_attn_rows_kernel(PagedAt
   griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int g = lane >> 2, c = lane & 3;
-  const int hk = blockIdx.y, z = blockIdx.z;
-  // (what returns here returns in every CTA of a cluster)
-  const SeqItem it = find_item(a.q, static_cast<int>(blockIdx.x), a.G, 4, 1);
-  if (it.seq < 0) return;
-  const int n = it.n;
-  if (n == 0) return;
-  if (n < 0 || it.row0 < 0 || n > a.q.n_tok - it.row0) {
-    if (threadIdx.x == 0) record_error(a.err, DEV_BAD_INDEX);
-    return;
+  const bool stream = a.plan.stream != 0;
+  int seq = 0, hk = blockIdx.y, tile = 0;
+  RowsSeq sq;
+  // a stretch [u, u_end) of the line of blocks; `before`: the blocks of the sequences ahead of `seq`
+  int64_t u = 0, u_begin = 0, u_end = 0, before = 0, line = 0, n_cta = 1;
+  if (stream) {
+    for (int s0 = 0; s0 < a.q.n_seq; s0 += 32) {
+      int64_t w = 0;
+      if (s0 + lane < a.q.n_seq) w = rows_units(a, rows_seq(a, s0 + lane));
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
+      line += w;
+    }
+    n_cta = min(static_cast<int64_t>(gridDim.x), line);  // nobody's stretch is empty
+    if (blockIdx.x >= n_cta) return;
+    u_begin = u = line * blockIdx.x / n_cta;
+    u_end = line * (blockIdx.x + 1) / n_cta;
+    for (int s0 = 0;; s0 += 32) {
+      int64_t w = 0;
+      if (s0 + lane < a.q.n_seq) w = rows_units(a, rows_seq(a, s0 + lane));
+      int64_t upto = w;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += x;
+      }
+      const unsigned past = __ballot_sync(0xffffffffu, before + upto > u);
+      if (past) {
+        const int l = __ffs(past) - 1;
+        seq = s0 + l;
+        before += __shfl_sync(0xffffffffu, upto - w, l);
+        break;
+      }
+      before += __shfl_sync(0xffffffffu, upto, 31);
+    }
+    sq = rows_seq(a, seq);
+  } else {
+    // (what returns here returns in every CTA of a cluster)
+    const SeqItem it = find_item(a.q, static_cast<int>(blockIdx.x), a.G, 4, 1);
+    if (it.seq < 0) return;
+    seq = it.seq;
+    tile = it.local;
+    sq = rows_seq(a, seq);
+    if (tile >= sq.tiles) return;
   }
-  int len = a.q.kv_len[it.seq];
-  if (len < 0 || len > kMaxLen || len > static_cast<int64_t>(a.q.table_stride) << a.c.page_log2) {
-    if (threadIdx.x == 0) record_error(a.err, DEV_BAD_INDEX);
-    len = 0;
+  for (;;) {
+  int range0 = 0, range1 = 0, slot = -1;  // blocks of the item; where its state goes
+  if (stream) {
+    while (u >= before + rows_units(a, sq)) {
+      before += rows_units(a, sq);
+      sq = rows_seq(a, ++seq);
+    }
+    const int64_t at = u - before;
+    const int64_t item = at / sq.blocks;
+    hk = static_cast<int>(item / sq.tiles);
+    tile = static_cast<int>(item % sq.tiles);
+    range0 = static_cast<int>(at - item * sq.blocks);
+    range1 = static_cast<int>(min(static_cast<int64_t>(sq.blocks), range0 + (u_end - u)));
+    if (range0 > 0 || range1 < sq.blocks) slot = 2 * blockIdx.x + (u == u_begin ? 0 : 1);
   }
+  const int n = sq.n, len = sq.len;
   const int R = n * a.G;
-  if (it.local >= (R + 15) >> 4) return;
-  const int r0 = it.local * 16;
+  const int r0 = tile * 16;
   const int r_end = min(r0 + 16, R);
   const bool upper = r_end - r0 > 8;  // rows 8 .. 15 exist
   // keys seen by a row: all, or up to its own position
@@ -247,14 +323,17 @@ __global__ void __launch_bounds__(kWarps * 32, 3) paged_attn_rows_kernel(PagedAt
   auto seen = [&](int r) { return a.causal ? first + min(r, R - 1) / a.G : len; };
   const int kmax = max(0, seen(r_end - 1));
   const int kmin = max(0, seen(r0));
-  // this item's blocks in even ranges, whole rounds of the warps
   const int bl = (kmax + 15) >> 4;
-  const int per = ((bl + a.plan.n_splits - 1) / a.plan.n_splits + kWarps - 1) / kWarps * kWarps;
-  const int b0 = min(bl, z * per), b1 = min(bl, b0 + per);
+  if (!stream) {  // even ranges, whole rounds of the warps
+    const int per = ((bl + a.plan.n_splits - 1) / a.plan.n_splits + kWarps - 1) / kWarps * kWarps;
+    range0 = static_cast<int>(blockIdx.z) * per;
+    range1 = range0 + per;
+  }
+  const int b0 = min(bl, range0), b1 = min(bl, range1);
   const int nb = b1 > b0 + warp ? (b1 - b0 - warp + kWarps - 1) / kWarps : 0;  // blocks of this warp
 
   // ---- page ids and constants of 32 of this warp's blocks at a time, one to a lane
-  const int32_t* tab = a.q.table + static_cast<int64_t>(it.seq) * a.q.table_stride;
+  const int32_t* tab = a.q.table + static_cast<int64_t>(seq) * a.q.table_stride;
   auto block_at = [&](int i) { return b0 + warp + i * kWarps; };
   auto fetch_ids = [&](int i0) {
     const int i = i0 + lane;
@@ -330,7 +409,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) paged_attn_rows_kernel(PagedAt
     const int r = r0 + g + 8 * e;
     vis[e] = seen(r);
     const bool ok = r < R;
-    const int tok = it.row0 + (ok ? r : r0) / a.G, hq = hk * a.G + (ok ? r : r0) % a.G;
+    const int tok = sq.row0 + (ok ? r : r0) / a.G, hq = hk * a.G + (ok ? r : r0) % a.G;
     const T* src = static_cast<const T*>(a.x) + tok * a.x_tok + hq * a.x_head;
     const bool wide = (reinterpret_cast<uintptr_t>(src) & 7) == 0;
     alignas(8) T v[D / 16][4];
@@ -360,8 +439,13 @@ __global__ void __launch_bounds__(kWarps * 32, 3) paged_attn_rows_kernel(PagedAt
     qs[e] = row_power<T>(am, &down) * a.scale_log2;
 #pragma unroll
     for (int t = 0; t < D / 16; ++t) {
-      qf[t][e] = pack2(to_f(v[t][0]) * down, to_f(v[t][1]) * down);
-      qf[t][2 + e] = pack2(to_f(v[t][2]) * down, to_f(v[t][3]) * down);
+      if (std::is_same<T, __half>::value) {
+        qf[t][e] = reinterpret_cast<const uint32_t*>(v[t])[0];
+        qf[t][2 + e] = reinterpret_cast<const uint32_t*>(v[t])[1];
+      } else {
+        qf[t][e] = pack2(to_f(v[t][0]) * down, to_f(v[t][1]) * down);
+        qf[t][2 + e] = pack2(to_f(v[t][2]) * down, to_f(v[t][3]) * down);
+      }
     }
   }
 
@@ -487,12 +571,15 @@ __global__ void __launch_bounds__(kWarps * 32, 3) paged_attn_rows_kernel(PagedAt
   float2* ml = reinterpret_cast<float2*>(smem + C::kRedMl);
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
+    if (e == 1 && !upper) break;
     const int r = g + 8 * e;
     if (c == 0) ml[warp * 16 + r] = make_float2(row_m[e], row_l[e]);
 #pragma unroll
-    for (int t = 0; t < D / 8; ++t)  // accumulator column 2c + i is lane group 2c + i's channel
+    for (int t = 0; t < D / 8; t += 2)  // accumulator column 2c + i is lane group 2c + i's channel
 #pragma unroll
-      for (int i = 0; i < 2; ++i) red[(warp * 16 + r) * C::kRedLd + (2 * c + i) * (D / 8) + t] = o[t][2 * e + i];
+      for (int i = 0; i < 2; ++i)
+        *reinterpret_cast<float2*>(&red[(warp * 16 + r) * C::kRedLd + (2 * c + i) * (D / 8) + t]) =
+            make_float2(o[t][2 * e + i], o[t + 1][2 * e + i]);
   }
   __syncthreads();
   const bool cluster = a.plan.cluster != 0;
@@ -508,15 +595,38 @@ __global__ void __launch_bounds__(kWarps * 32, 3) paged_attn_rows_kernel(PagedAt
     if (cluster) {  // warp 0's rows now hold the CTA's: each thread read what it overwrites
       *reinterpret_cast<float4*>(red + r * C::kRedLd + d) = st.o;
       if (d == 0) ml[kWarps * 16 + r] = make_float2(st.M, st.L);
-    } else {
-      const int rr = r0 + r;
-      finish_row<T>(a, st, a.plan.n_splits > 1, z, it.row0 + rr / a.G, hk * a.G + rr % a.G, d);
+      continue;
     }
+    const int rr = r0 + r, tok = sq.row0 + rr / a.G, hq = hk * a.G + rr % a.G;
+    if (slot < 0) {
+      finish_row<T>(a, st, tok, hq, d);
+    } else {
+      const int64_t p = static_cast<int64_t>(slot) * 16 + r;
+      *reinterpret_cast<float4*>(a.part_o + p * D + d) = st.o;
+      if (d == 0) a.part_ml[p] = make_float2(st.M, st.L);
+    }
+    // the CTA of an item's first blocks says where the row's parts are
+    if (stream && range0 == 0 && d == 0) {
+      int parts = 0;
+      if (slot >= 0) {
+        const int64_t end = u + sq.blocks;  // the line's end of this item: the CTA of its last block
+        int last = static_cast<int>(min(n_cta - 1, end * n_cta / line));
+        while (line * last / n_cta >= end) --last;
+        parts = last - static_cast<int>(blockIdx.x) + 1;
+      }
+      a.part_at[static_cast<int64_t>(tok) * a.Hq + hq] = make_int2(slot * 16 + r, parts);
+    }
+  }
+  if (stream) {
+    u += range1 - range0;
+    if (u >= u_end) return;
+    __syncthreads();  // the ring reuses what the join read
+    continue;
   }
   if (!cluster) return;
   cluster_sync_all();
   const int nz = a.plan.n_splits;
-  for (int x = z * kWarps * 32 + threadIdx.x; x < work; x += nz * kWarps * 32) {
+  for (int x = blockIdx.z * kWarps * 32 + threadIdx.x; x < work; x += nz * kWarps * 32) {
     const int r = x / (D / 4), d = (x % (D / 4)) * 4;
     RowState st;
     float2 m[8];
@@ -527,42 +637,108 @@ __global__ void __launch_bounds__(kWarps * 32, 3) paged_attn_rows_kernel(PagedAt
     for (int q = 0; q < 8; ++q)
       if (q < nz) st.add(m[q], dsmem_ld_f4(dsmem_addr(red + r * C::kRedLd + d, q)));
     const int rr = r0 + r;
-    finish_row<T>(a, st, false, 0, it.row0 + rr / a.G, hk * a.G + rr % a.G, d);
+    finish_row<T>(a, st, sq.row0 + rr / a.G, hk * a.G + rr % a.G, d);
   }
   cluster_sync_all();  // no CTA leaves while another reads its shared memory
+  return;
+  }
 }
 
-// Joins the key ranges of a row: out = sum 2^(M_i - M) O_i / sum 2^(M_i - M) l_i.
+// Joins the parts of a row, one CTA each: out = sum 2^(M_i - M) O_i / sum
+// 2^(M_i - M) l_i.  With ranges, part i is range i's state of the row; with
+// stretches, the first part is where part_at says and the others begin the
+// stretches of the CTAs after it.  A warp takes 32 parts at a time, one (M, l) to a
+// lane, then their O rows one after the other with the loads in flight
+// together.
+constexpr int kJoinWarps = 4;
 template <int D, class T>
-__global__ void __launch_bounds__(256) paged_attn_join_kernel(PagedAttnArgs a) {
+__global__ void __launch_bounds__(kJoinWarps * 32) paged_attn_join_kernel(PagedAttnArgs a) {
   griddep_launch_dependents();
   griddep_wait();
-  constexpr int kPer = D / 4;  // threads of a row
-  const int64_t row = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) / kPer;
-  const int d = (threadIdx.x % kPer) * 4;
-  const int64_t rows = static_cast<int64_t>(a.q.n_tok) * a.Hq;
-  if (row >= rows) return;
-  const int tok = static_cast<int>(row / a.Hq), hq = static_cast<int>(row % a.Hq);
+  constexpr int kV = D / 32;  // channels of a lane
+  const int row = blockIdx.x;
+  const int tok = row / a.Hq, hq = row % a.Hq;
   if (tok < a.q.q_off[0] || tok >= a.q.q_off[a.q.n_seq]) return;  // rows of no sequence stay as they are
-  RowState st;
-  for (int z = 0; z < a.plan.n_splits; ++z) st.top(a.part_ml[z * rows + row]);
-  for (int z = 0; z < a.plan.n_splits; ++z) {
-    const float2 ml = a.part_ml[z * rows + row];
-    if (ml.y == 0.f) continue;
-    st.add(ml, *reinterpret_cast<const float4*>(a.part_o + (z * rows + row) * D + d));
+  int2 at = make_int2(0, a.plan.n_splits);
+  if (a.plan.stream) {
+    at = a.part_at[row];
+    // (rows between bad offsets were never described: what stands there is not followed out of range)
+    const int cta = at.x >> 5;
+    if (at.x < 0 || at.y < 1 || cta >= a.plan.n_splits || at.y > a.plan.n_splits - cta) return;
   }
-  finish_row<T>(a, st, false, 0, tok, hq, d);
+  const int64_t rows = static_cast<int64_t>(a.q.n_tok) * a.Hq;
+  auto part = [&](int i) {
+    if (!a.plan.stream) return i * rows + row;
+    return static_cast<int64_t>(i == 0 ? at.x : ((at.x >> 5) + i) * 32 + (at.x & 15));
+  };
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  float M = -INFINITY, L = 0.f, o[kV];
+#pragma unroll
+  for (int k = 0; k < kV; ++k) o[k] = 0.f;
+  for (int i0 = warp * 32; i0 < at.y; i0 += kJoinWarps * 32) {
+    const int n = min(32, at.y - i0);
+    const float2 ml = lane < n ? a.part_ml[part(i0 + lane)] : make_float2(-INFINITY, 0.f);
+    float m = ml.y != 0.f ? ml.x : -INFINITY;
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, s));
+    m = fmaxf(m, M);
+    const float f = M == -INFINITY ? 0.f : ex2_approx(M - m);
+    M = m;
+    L *= f;
+#pragma unroll
+    for (int k = 0; k < kV; ++k) o[k] *= f;
+    const float w = ml.y != 0.f ? ex2_approx(ml.x - m) : 0.f;
+    L = fmaf(w, ml.y, L);  // of this lane's parts
+    const unsigned some = __ballot_sync(0xffffffffu, ml.y != 0.f);
+#pragma unroll 8
+    for (int j = 0; j < n; ++j) {
+      const float wj = __shfl_sync(0xffffffffu, w, j);
+      const float* src = a.part_o + part(i0 + j) * D + lane * kV;
+      float v[kV];
+#pragma unroll
+      for (int k = 0; k < kV; ++k) v[k] = some >> j & 1 ? src[k] : 0.f;  // an empty part has no O
+#pragma unroll
+      for (int k = 0; k < kV; ++k) o[k] = fmaf(wj, v[k], o[k]);
+    }
+  }
+#pragma unroll
+  for (int s = 16; s > 0; s >>= 1) L += __shfl_xor_sync(0xffffffffu, L, s);
+  __shared__ float2 sml[kJoinWarps];
+  __shared__ __align__(16) float so[kJoinWarps][D];
+  if (lane == 0) sml[warp] = make_float2(M, L);
+#pragma unroll
+  for (int k = 0; k < kV; ++k) so[warp][lane * kV + k] = o[k];
+  __syncthreads();
+  if (threadIdx.x >= D / 4) return;
+  const int d = threadIdx.x * 4;
+  RowState st;
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) st.top(sml[w]);
+#pragma unroll
+  for (int w = 0; w < kJoinWarps; ++w) st.add(sml[w], *reinterpret_cast<const float4*>(&so[w][d]));
+  finish_row<T>(a, st, tok, hq, d);
+}
+
+template <int D, class T>
+int launch_join(const PagedAttnArgs& a, cudaStream_t s) {
+  auto kern = paged_attn_join_kernel<D, T>;
+  static KernelSetup setup;
+  const cudaError_t r = setup.run(kern, 0);
+  if (r != cudaSuccess) return r;
+  return launch_k(kern, dim3(static_cast<unsigned>(a.q.n_tok * a.Hq)), dim3(kJoinWarps * 32), 0, s, a);
 }
 
 template <int D, int FMT, class T>
 int launch_rows(const PagedAttnArgs& a, cudaStream_t s) {
   using C = RowsCfg<D>;
   auto kern = paged_attn_rows_kernel<D, FMT, T>;
-  const cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  static KernelSetup setup;
+  const cudaError_t r = setup.run(kern, C::kSmem);
   if (r != cudaSuccess) return r;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(((static_cast<int64_t>(a.q.n_tok) * a.G) >> 4) + a.q.n_seq),
-                     static_cast<unsigned>(a.c.Hkv), static_cast<unsigned>(a.plan.n_splits));
+  cfg.gridDim = a.plan.stream ? dim3(static_cast<unsigned>(a.plan.n_splits))
+                              : dim3(static_cast<unsigned>(((static_cast<int64_t>(a.q.n_tok) * a.G) >> 4) + a.q.n_seq),
+                                     static_cast<unsigned>(a.c.Hkv), static_cast<unsigned>(a.plan.n_splits));
   cfg.blockDim = dim3(kWarps * 32);
   cfg.dynamicSmemBytes = C::kSmem;
   cfg.stream = s;
@@ -596,15 +772,24 @@ void plan_paged_attention(int n_tok, int n_seq, int G, int Hkv, int64_t max_kv, 
   const int64_t per = n_seq > 0 ? (n_tok + n_seq - 1) / n_seq : 0;  // query tokens of a sequence, on average
   p->rows = per * G > 32 ? 256 : 16;
   const int64_t tiles = std::max<int64_t>(1, n_seq * ((per * G + p->rows - 1) / p->rows) * Hkv);
+  const int64_t slots = static_cast<int64_t>(sms) * 3;  // resident CTAs of the rows kernel
+  p->stream = p->cluster = 0;
   int64_t want;
   if (p->rows == 16) {
-    want = std::min((static_cast<int64_t>(sms) * 12 + tiles - 1) / tiles, (max_kv + 63) / 64);
-    p->cluster = want > 1 && want <= 8;
+    // Ranges for about 7/4 CTAs a slot, at most a cluster's 8; the even
+    // stretches where each is long (over 3000 keys: 64 x 8 k keys take 111 us
+    // against 117 in ranges, 64 x 2 k, 1100 keys each, 51 against 47), or where
+    // 8 ranges leave most SMs idle and each is longer than the stretches' own
+    // 15 us of set-up and joining are worth (1 x 4 k keys: 13 us in a cluster
+    // against 20; 1 x 16 k: 31 against 25).
+    want = std::max<int64_t>(1, slots * 7 / 4 / tiles);
+    p->stream = n_seq <= 4096 && (tiles * max_kv >= slots * 3000 || (want > 8 && max_kv > 10240));
+    want = p->stream ? slots : std::min<int64_t>(std::min<int64_t>(want, 8), (max_kv + 63) / 64);
+    p->cluster = !p->stream && want > 1;
   } else {
     want = std::min<int64_t>(sms / tiles, (max_kv + 127) / 128);
-    p->cluster = 0;
   }
-  p->n_splits = static_cast<int>(std::min<int64_t>(std::max<int64_t>(want, 1), 256));
+  p->n_splits = static_cast<int>(std::max<int64_t>(want, 1));
 }
 
 int launch_paged_attention(const PagedAttnArgs& a, cudaStream_t s) {
@@ -618,14 +803,9 @@ int launch_paged_attention(const PagedAttnArgs& a, cudaStream_t s) {
   else
     r = f8 ? launch_rows_t<128, PCD_KV_E4M3>(a, s) : launch_rows_t<128, PCD_KV_INT8>(a, s);
   if (r != 0 || a.plan.n_splits == 1 || a.plan.cluster) return r;
-  const int64_t threads = static_cast<int64_t>(a.q.n_tok) * a.Hq * (a.c.dim / 4);
-  const dim3 grid(static_cast<unsigned>((threads + 255) / 256));
   const bool bf = a.dtype == PCD_DTYPE_BF16;
-  if (a.c.dim == 64)
-    return bf ? launch_k(paged_attn_join_kernel<64, __nv_bfloat16>, grid, dim3(256), 0, s, a)
-              : launch_k(paged_attn_join_kernel<64, __half>, grid, dim3(256), 0, s, a);
-  return bf ? launch_k(paged_attn_join_kernel<128, __nv_bfloat16>, grid, dim3(256), 0, s, a)
-            : launch_k(paged_attn_join_kernel<128, __half>, grid, dim3(256), 0, s, a);
+  if (a.c.dim == 64) return bf ? launch_join<64, __nv_bfloat16>(a, s) : launch_join<64, __half>(a, s);
+  return bf ? launch_join<128, __nv_bfloat16>(a, s) : launch_join<128, __half>(a, s);
 }
 
 }  // namespace pcd

@@ -3,6 +3,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
+#include <atomic>
 #include <cstdint>
 #include <type_traits>
 
@@ -32,6 +33,27 @@ __device__ __forceinline__ void turn(int p, int64_t F, float* c, float* s) {
   const uint64_t phase = static_cast<uint64_t>(static_cast<int64_t>(p)) * static_cast<uint64_t>(F);
   sincospif(static_cast<float>(static_cast<int32_t>(phase >> 32)) * 4.656612873077393e-10f /* 2^-31: half turns */, s, c);
 }
+
+// Attributes of a kernel, set once a device (a static of its launcher): its
+// dynamic shared memory, and an SM split all for shared memory.  An SM that
+// last ran a kernel without shared memory keeps its split while CTAs are on
+// it, and would hold fewer of these than fit.
+struct KernelSetup {
+  std::atomic<uint64_t> done{0};
+  template <class Kern>
+  cudaError_t run(Kern kern, int smem) {
+    int dev = 0;
+    cudaError_t r = cudaGetDevice(&dev);
+    if (r != cudaSuccess) return r;
+    const uint64_t bit = uint64_t{1} << (dev & 63);
+    if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    if (smem > 0) r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (r == cudaSuccess)
+      r = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+    if (r == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    return r;
+  }
+};
 
 // ------------------------------------------------------------------ sequences
 constexpr int kMaxLen = 0x7ffffc00;  // tokens of a sequence: positions and their roundings stay in 32 bits
@@ -162,16 +184,9 @@ struct RowState {
     o.w = fmaf(w, v.w, o.w);
   }
 };
-// Writes 4 channels of a row: the output, or the partial of key range z.
+// Writes 4 channels of an output row, and its log-sum-exp.
 template <class T>
-__device__ __forceinline__ void finish_row(const PagedAttnArgs& a, const RowState& st, bool partial, int z, int tok, int hq,
-                                           int d) {
-  if (partial) {
-    const int64_t row = (static_cast<int64_t>(z) * a.q.n_tok + tok) * a.Hq + hq;
-    if (d == 0) a.part_ml[row] = make_float2(st.M, st.L);
-    if (st.L != 0.f) *reinterpret_cast<float4*>(a.part_o + row * a.c.dim + d) = st.o;
-    return;
-  }
+__device__ __forceinline__ void finish_row(const PagedAttnArgs& a, const RowState& st, int tok, int hq, int d) {
   const float il = st.L == 0.f ? 0.f : 1.f / st.L;
   T* out = static_cast<T*>(a.out) + tok * a.out_tok + hq * a.out_head + d;
   out[0] = from_f<T>(st.o.x * il);

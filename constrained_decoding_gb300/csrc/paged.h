@@ -58,11 +58,12 @@ struct AppendArgs {
 };
 int launch_kv_append(const AppendArgs& a, cudaStream_t s);
 
-// How a call is cut up: query rows of a work item (16: warp MMA, 256:
-// tcgen05) and the ranges that every item's keys are divided into; `cluster`:
-// a thread-block cluster walks the ranges of an item and joins them itself.
+// How a call is cut up.  rows: query rows of a work item (16: warp MMA, 256:
+// tcgen05).  n_splits: ranges that every item's keys are divided into, walked
+// by a thread-block cluster that joins them (cluster) or joined by a second
+// kernel; with stream, CTAs that share the blocks of all items evenly.
 struct PagedPlan {
-  int rows, n_splits, cluster;
+  int rows, n_splits, cluster, stream;
 };
 
 struct PagedAttnArgs {
@@ -75,8 +76,11 @@ struct PagedAttnArgs {
   int64_t x_tok, x_head, out_tok, out_head;  // elements
   float scale_log2;                          // softmax scale x log2(e)
   PagedPlan plan;
-  float* part_o;                             // [n_splits][n_tok][Hq][dim], when ranges are joined by a second kernel
-  float2* part_ml;                           // [n_splits][n_tok][Hq]
+  // scratch: states (O, then M and l) of rows cut by ranges, [n_splits][n_tok][Hq], or by the ends of
+  // stretches, [2 n_splits][16], and then where a row's are
+  float* part_o;
+  float2* part_ml;
+  int2* part_at;
   int* err;
 };
 void plan_paged_attention(int n_tok, int n_seq, int G, int Hkv, int64_t max_kv, int sms, PagedPlan* p);

@@ -199,9 +199,13 @@ extern "C" int pcd_k_kv_append(const pcd_kv_pages* cache, const void* k, const v
 }
 
 namespace {
+// Rows of partial states in scratch, and rows that say where theirs are.
+int64_t attn_parts(int n_tok, int Hq, const pcd::PagedPlan& p) {
+  if (p.stream) return static_cast<int64_t>(p.n_splits) * 2 * 16;
+  return p.n_splits <= 1 || p.cluster ? 0 : static_cast<int64_t>(p.n_splits) * n_tok * Hq;
+}
 int64_t attn_scratch(int n_tok, int Hq, int dim, const pcd::PagedPlan& p) {
-  if (p.n_splits <= 1 || p.cluster) return 0;
-  return static_cast<int64_t>(p.n_splits) * n_tok * Hq * (dim * 4 + 8);
+  return attn_parts(n_tok, Hq, p) * (dim * 4 + 8) + (p.stream ? static_cast<int64_t>(n_tok) * Hq * 8 : 0);
 }
 }  // namespace
 
@@ -250,8 +254,10 @@ extern "C" int pcd_k_paged_attention(const pcd_kv_pages* cache, const void* q, v
   if (need > 0) {
     PCD_REFUSE(!scratch || !aligned(scratch, 16) || scratch_bytes < need, PCD_ERR_INVALID_ARG,
                "scratch is smaller than pcd_k_paged_attention_scratch_bytes, or unaligned");
+    const int64_t parts = attn_parts(n_tok, n_q_heads, a.plan);
     a.part_o = static_cast<float*>(scratch);
-    a.part_ml = reinterpret_cast<float2*>(a.part_o + static_cast<int64_t>(a.plan.n_splits) * n_tok * n_q_heads * a.c.dim);
+    a.part_ml = reinterpret_cast<float2*>(a.part_o + parts * a.c.dim);
+    a.part_at = reinterpret_cast<int2*>(a.part_ml + parts);
   }
   return launched(pcd::launch_paged_attention(a, static_cast<cudaStream_t>(stream)));
 }

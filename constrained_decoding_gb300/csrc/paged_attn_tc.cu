@@ -495,7 +495,8 @@ template <int D, int FMT, class T>
 int launch_tile(const PagedAttnArgs& a, cudaStream_t s) {
   using C = TileCfg<D>;
   auto kern = paged_attn_tile_kernel<D, FMT, T>;
-  cudaError_t r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+  static KernelSetup setup;
+  const cudaError_t r = setup.run(kern, C::kSmem);
   if (r != cudaSuccess) return r;
   const int64_t items = ((static_cast<int64_t>(a.q.n_tok) * a.G) >> 8) + a.q.n_seq;
   return launch_k(kern, dim3(static_cast<unsigned>(items), static_cast<unsigned>(a.c.Hkv), static_cast<unsigned>(a.plan.n_splits)),
