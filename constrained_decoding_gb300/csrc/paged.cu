@@ -18,46 +18,117 @@ namespace {
 
 // ======================================================================== rope
 // y = R x per pair; the angle is p F mod 1 turn in 64-bit integers, so it is
-// as exact at position 2^31 as at 1.  One thread a pair.
-template <class T>
-__global__ void rope_kernel(RopeKArgs a) {
+// as exact at position 2^31 as at 1.  Bound by the bytes of x and y: a thread
+// owns the same VEC channels (and their partners, rot / 2 further, in the half
+// layout) of every hgs-th head of one token, so an angle's sine and cosine are
+// computed once for all of them, and takes four heads' loads at a time.
+// VEC: the widest access that pointers, strides and the pair layout allow.
+template <class T, int N>
+struct alignas(sizeof(T) * N) Chunk {
+  T v[N];
+};
+template <class T, int VEC, bool INTER>
+__global__ void __launch_bounds__(256) rope_kernel(RopeKArgs a, unsigned units, unsigned rot_units, unsigned hgs,
+                                                   unsigned total) {
+  constexpr int kN = INTER && VEC == 1 ? 2 : VEC;   // channels of a chunk of the rotated part
+  constexpr int kL = INTER && VEC == 1 ? 1 : VEC;   // channels of one access
+  constexpr int kPairs = INTER ? kN / 2 : kN;
+  constexpr int kHeads = 4;
   griddep_launch_dependents();
   griddep_wait();
-  const int half = a.rope.rot / 2, rest = a.dim - a.rope.rot;
-  const int units = half + rest;
-  const int64_t idx = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  const int64_t total = static_cast<int64_t>(a.n_tok) * a.heads * units;
+  const unsigned idx = blockIdx.x * 256u + threadIdx.x;
   if (idx >= total) return;
-  const int u = static_cast<int>(idx % units);
-  const int64_t th = idx / units;
-  const int h = static_cast<int>(th % a.heads);
-  const int64_t t = th / a.heads;
-  const T* x = static_cast<const T*>(a.x) + t * a.x_tok + h * a.x_head;
-  T* y = static_cast<T*>(a.y) + t * a.y_tok + h * a.y_head;
-  if (u >= half) {
-    y[a.rope.rot + u - half] = x[a.rope.rot + u - half];
+  const unsigned u = idx % units, th = idx / units;
+  const int hg = static_cast<int>(th % hgs), t = static_cast<int>(th / hgs);
+  const T* x = static_cast<const T*>(a.x) + t * a.x_tok;
+  T* y = static_cast<T*>(a.y) + t * a.y_tok;
+  if (u >= rot_units) {  // a chunk that is copied
+    const int d = a.rope.rot + static_cast<int>(u - rot_units) * VEC;
+    for (int h = hg; h < a.heads; h += static_cast<int>(hgs))
+      *reinterpret_cast<Chunk<T, VEC>*>(y + h * a.y_head + d) = *reinterpret_cast<const Chunk<T, VEC>*>(x + h * a.x_head + d);
     return;
   }
-  float c, s;
-  turn(a.pos ? a.pos[t] : a.base + static_cast<int>(t), a.rope.freqs[u], &c, &s);
-  c *= a.rope.amp;
-  s *= a.rope.transpose ? -a.rope.amp : a.rope.amp;
-  const int i = a.rope.interleaved ? 2 * u : u, j = a.rope.interleaved ? 2 * u + 1 : u + half;
-  const float p = to_f(x[i]), q = to_f(x[j]);
-  y[i] = from_f<T>(p * c - q * s);
-  y[j] = from_f<T>(q * c + p * s);
+  const int pair = static_cast<int>(u) * kPairs;
+  const int d = static_cast<int>(u) * kN, half = a.rope.rot / 2;
+  const int p = a.pos ? a.pos[t] : a.base + t;
+  float c[kPairs], s[kPairs];
+#pragma unroll
+  for (int i = 0; i < kPairs; ++i) {
+    turn(p, a.rope.freqs[pair + i], &c[i], &s[i]);
+    c[i] *= a.rope.amp;
+    s[i] *= a.rope.transpose ? -a.rope.amp : a.rope.amp;
+  }
+  using C = Chunk<T, kL>;
+  for (int h0 = hg; h0 < a.heads; h0 += kHeads * static_cast<int>(hgs)) {
+    C v[kHeads][INTER ? kN / kL : 2];
+#pragma unroll
+    for (int k = 0; k < kHeads; ++k) {
+      const int h = h0 + k * static_cast<int>(hgs);
+      if (h >= a.heads) break;
+      const T* r = x + h * a.x_head + d;
+#pragma unroll
+      for (int j = 0; j < (INTER ? kN / kL : 2); ++j) v[k][j] = *reinterpret_cast<const C*>(r + (INTER ? j * kL : j * half));
+    }
+#pragma unroll
+    for (int k = 0; k < kHeads; ++k) {
+      const int h = h0 + k * static_cast<int>(hgs);
+      if (h >= a.heads) break;
+#pragma unroll
+      for (int i = 0; i < kPairs; ++i) {
+        T& e0 = INTER ? v[k][2 * i / kL].v[2 * i % kL] : v[k][0].v[i];
+        T& e1 = INTER ? v[k][(2 * i + 1) / kL].v[(2 * i + 1) % kL] : v[k][1].v[i];
+        const float f0 = to_f(e0), f1 = to_f(e1);
+        e0 = from_f<T>(f0 * c[i] - f1 * s[i]);
+        e1 = from_f<T>(f1 * c[i] + f0 * s[i]);
+      }
+      T* r = y + h * a.y_head + d;
+#pragma unroll
+      for (int j = 0; j < (INTER ? kN / kL : 2); ++j) *reinterpret_cast<C*>(r + (INTER ? j * kL : j * half)) = v[k][j];
+    }
+  }
+}
+
+template <class T, int VEC>
+int launch_rope_v(const RopeKArgs& a, int sms, cudaStream_t s) {
+  const bool inter = a.rope.interleaved != 0;
+  const int rot_units = inter ? a.rope.rot / std::max(VEC, 2) : a.rope.rot / 2 / VEC;
+  // in place, the channels behind the rotated ones already stand where they belong
+  const int units = rot_units + (a.x == a.y ? 0 : (a.dim - a.rope.rot) / VEC);
+  if (units == 0) return 0;
+  // as few head groups as fill the GPU's threads
+  const int64_t per_group = static_cast<int64_t>(a.n_tok) * units;
+  const int64_t fill = (static_cast<int64_t>(sms) * 2048 + per_group - 1) / per_group;
+  const int64_t hgs = std::min<int64_t>(a.heads, std::max<int64_t>(1, fill));
+  const int64_t total = per_group * hgs;
+  if (total >= (int64_t{1} << 31)) return cudaErrorInvalidValue;
+  const dim3 grid(static_cast<unsigned>((total + 255) / 256));
+  auto kern = inter ? rope_kernel<T, VEC, true> : rope_kernel<T, VEC, false>;
+  return launch_k(kern, grid, dim3(256), 0, s, a, static_cast<unsigned>(units), static_cast<unsigned>(rot_units),
+                  static_cast<unsigned>(hgs), static_cast<unsigned>(total));
+}
+
+template <class T>
+int launch_rope_t(const RopeKArgs& a, int sms, cudaStream_t s) {
+  // every chunk starts at a multiple of these, in elements
+  uint64_t m = static_cast<uint64_t>(a.dim) | static_cast<uint64_t>(a.rope.rot);
+  m |= a.rope.interleaved ? 0 : static_cast<uint64_t>(a.rope.rot / 2);
+  if (a.n_tok > 1) m |= static_cast<uint64_t>(a.x_tok) | static_cast<uint64_t>(a.y_tok);
+  if (a.heads > 1) m |= static_cast<uint64_t>(a.x_head) | static_cast<uint64_t>(a.y_head);
+  m |= (reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.y)) / sizeof(T);
+  if (sizeof(T) == 2 && m % 8 == 0) return launch_rope_v<T, 16 / sizeof(T)>(a, sms, s);
+  if (m % 4 == 0) return launch_rope_v<T, 4>(a, sms, s);
+  if (m % 2 == 0) return launch_rope_v<T, 2>(a, sms, s);
+  return launch_rope_v<T, 1>(a, sms, s);
 }
 
 }  // namespace
 
-int launch_rope(const RopeKArgs& a, cudaStream_t s) {
+int launch_rope(const RopeKArgs& a, int sms, cudaStream_t s) {
   if (a.n_tok == 0 || a.heads == 0) return 0;
-  const int64_t total = static_cast<int64_t>(a.n_tok) * a.heads * (a.dim - a.rope.rot / 2);
-  const dim3 grid(static_cast<unsigned>((total + 255) / 256));
   switch (a.dtype) {
-    case PCD_DTYPE_F32: return launch_k(rope_kernel<float>, grid, dim3(256), 0, s, a);
-    case PCD_DTYPE_BF16: return launch_k(rope_kernel<__nv_bfloat16>, grid, dim3(256), 0, s, a);
-    default: return launch_k(rope_kernel<__half>, grid, dim3(256), 0, s, a);
+    case PCD_DTYPE_F32: return launch_rope_t<float>(a, sms, s);
+    case PCD_DTYPE_BF16: return launch_rope_t<__nv_bfloat16>(a, sms, s);
+    default: return launch_rope_t<__half>(a, sms, s);
   }
 }
 
@@ -95,85 +166,188 @@ __device__ __forceinline__ float append_value(const AppendArgs& a, bool is_v, co
   return second ? q * c + p * s : p * c - q * s;
 }
 
-template <class T>
-__global__ void __launch_bounds__(kAppendThreads) kv_append_kernel(AppendArgs a) {
-  griddep_launch_dependents();
-  griddep_wait();
+// The block of a CTA: its new rows and where they go.
+struct AppendBlock {
+  int held, rows, row0, pos0;  // older tokens in the page; new rows, the first one's index and position
+  uint8_t* dst;
+  float* scale;
+};
+__device__ __forceinline__ bool append_block(const AppendArgs& a, bool is_v, AppendBlock* b) {
   const int page = 1 << a.c.page_log2;
   const int h = blockIdx.y;
-  const bool is_v = blockIdx.z != 0;
-  const int tid = threadIdx.x, lane = tid & 31;
   // item -> (sequence, page of its new range)
   const SeqItem it = find_item(a.q, static_cast<int>(blockIdx.x), 1, a.c.page_log2, 2);
-  if (it.seq < 0) return;
+  if (it.seq < 0) return false;
   const int n = it.n, len = a.q.kv_len[it.seq];
-  if (n == 0) return;
+  if (n == 0) return false;
   if (n < 0 || it.row0 < 0 || n > a.q.n_tok - it.row0 || len < n || len > kMaxLen ||
       len > static_cast<int64_t>(a.q.table_stride) << a.c.page_log2) {
-    if (tid == 0) record_error(a.err, DEV_BAD_INDEX);
-    return;
+    if (threadIdx.x == 0) record_error(a.err, DEV_BAD_INDEX);
+    return false;
   }
-  if (it.local > (n >> a.c.page_log2) + 1) return;
+  if (it.local > (n >> a.c.page_log2) + 1) return false;
   const int start = len - n;
   const int pg = (start >> a.c.page_log2) + it.local;
   const int lo = max(pg << a.c.page_log2, start), hi = min((pg + 1) << a.c.page_log2, len);
-  if (lo >= hi) return;
+  if (lo >= hi) return false;
   const int id = a.q.table[static_cast<int64_t>(it.seq) * a.q.table_stride + pg];
   if (id < 0 || id >= a.c.n_pages) {
-    if (tid == 0) record_error(a.err, DEV_BAD_INDEX);
-    return;
+    if (threadIdx.x == 0) record_error(a.err, DEV_BAD_INDEX);
+    return false;
   }
-  const int held = lo & (page - 1), rows = hi - lo, D = a.c.dim;
-  const int t0 = it.row0 + (lo - start);
-  const T* src = static_cast<const T*>(is_v ? a.v : a.k) + (is_v ? a.v_head : a.k_head) * h;
-  const int64_t ts = is_v ? a.v_tok : a.k_tok;
-  uint8_t* dst = (is_v ? a.c.v : a.c.k) + id * a.c.page_stride + h * a.c.head_stride;
-  float* sc = (is_v ? a.c.vs : a.c.ks) + static_cast<int64_t>(id) * a.c.Hkv + h;
+  b->held = lo & (page - 1);
+  b->rows = hi - lo;
+  b->row0 = it.row0 + (lo - start);
+  b->pos0 = lo;
+  b->dst = (is_v ? a.c.v : a.c.k) + id * a.c.page_stride + h * a.c.head_stride;
+  b->scale = (is_v ? a.c.vs : a.c.ks) + static_cast<int64_t>(id) * a.c.Hkv + h;
+  return true;
+}
 
-  // |x| as integers: their order is the floats', and a NaN beats everything
-  uint32_t am = 0;
-  for (int e = tid; e < rows * D; e += kAppendThreads) {
-    const int r = e / D, d = e - r * D;
-    const int p = a.pos ? a.pos[t0 + r] : lo + r;
-    am = max(am, __float_as_uint(append_value(a, is_v, src + (t0 + r) * ts, d, p)) & 0x7fffffffu);
-  }
-  __shared__ uint32_t red[kAppendThreads / 32];
+// The block's scale from every thread's largest |x| (bits), written; the older
+// codes are brought to it if it grew.  |x| as integers: their order is the
+// floats', and a NaN beats everything.
+__device__ __forceinline__ float append_scale(const AppendArgs& a, const AppendBlock& b, uint32_t am) {
+  __shared__ uint32_t red[32];
+  const int tid = threadIdx.x, nw = blockDim.x >> 5;
   am = __reduce_max_sync(0xffffffffu, am);
-  if (lane == 0) red[tid >> 5] = am;
-  __syncthreads();
-#pragma unroll
-  for (int w = 0; w < kAppendThreads / 32; ++w) am = max(am, red[w]);
-  const float old = held ? *sc : 0.f;
-  const float scale = block_scale(__uint_as_float(am), old, held > 0, a.c.format);
+  if ((tid & 31) == 0) red[tid >> 5] = am;
+  const float old = b.held ? *b.scale : 0.f;
   __syncthreads();  // every thread has read the old scale
-  if (tid == 0) *sc = scale;
-  if (held && !(scale == old)) {
+  for (int w = 0; w < nw; ++w) am = max(am, red[w]);
+  const float scale = block_scale(__uint_as_float(am), old, b.held > 0, a.c.format);
+  if (tid == 0) *b.scale = scale;
+  if (b.held && !(scale == old)) {
     const float ratio = old / scale;
-    for (int e = tid; e < held * D; e += kAppendThreads) {
-      const int r = e / D, d = e - r * D;
-      uint8_t* q = dst + r * a.c.tok_stride + d;
-      *q = encode(decode(*q, a.c.format) * ratio, a.c.format);
+    const int per = a.c.dim / 4;
+    for (int e = tid; e < b.held * per; e += blockDim.x) {
+      const int r = e / per;
+      uint32_t* q = reinterpret_cast<uint32_t*>(b.dst + r * a.c.tok_stride + (e - r * per) * 4);
+      uint32_t w = *q, y = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        y |= static_cast<uint32_t>(encode(decode(static_cast<uint8_t>(w >> (8 * i)), a.c.format) * ratio, a.c.format)) << (8 * i);
+      *q = y;
     }
   }
-  const float inv = 1.f / scale;
-  for (int e = tid; e < rows * D; e += kAppendThreads) {
-    const int r = e / D, d = e - r * D;
-    const int p = a.pos ? a.pos[t0 + r] : lo + r;
-    dst[(held + r) * a.c.tok_stride + d] =
-        encode(append_value(a, is_v, src + (t0 + r) * ts, d, p) * inv, a.c.format);
+  return scale;
+}
+
+// Any layout: a channel at a time, each value computed for the maximum and
+// again for its code.
+template <class T>
+__global__ void __launch_bounds__(kAppendThreads) kv_append_any_kernel(AppendArgs a) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const bool is_v = blockIdx.z != 0;
+  AppendBlock b;
+  if (!append_block(a, is_v, &b)) return;
+  const int D = a.c.dim, total = b.rows * D;
+  const T* src = static_cast<const T*>(is_v ? a.v : a.k) + (is_v ? a.v_head : a.k_head) * blockIdx.y;
+  const int64_t ts = is_v ? a.v_tok : a.k_tok;
+  auto value = [&](int r, int d) {
+    return append_value(a, is_v, src + (b.row0 + r) * ts, d, a.pos ? a.pos[b.row0 + r] : b.pos0 + r);
+  };
+  uint32_t am = 0;
+  for (int e = threadIdx.x; e < total; e += kAppendThreads)
+    am = max(am, __float_as_uint(value(e / D, e % D)) & 0x7fffffffu);
+  const float inv = 1.f / append_scale(a, b, am);
+  for (int e = threadIdx.x; e < total; e += kAppendThreads)
+    b.dst[(b.held + e / D) * a.c.tok_stride + e % D] = encode(value(e / D, e % D) * inv, a.c.format);
+}
+
+__device__ __forceinline__ void append_turn(const RopeSpec& rope, int p, int pair, float& x, float& y) {
+  float c, s;
+  turn(p, rope.freqs[pair], &c, &s);
+  c *= rope.amp;
+  s *= rope.amp;
+  const float x0 = x, y0 = y;
+  x = x0 * c - y0 * s;
+  y = y0 * c + x0 * s;
+}
+
+// Rows of whole 16-byte chunks: a thread holds NU units of a row's 16 channels
+// (two 8-channel chunks, the partners of the half layout's pairs) in registers
+// between the maximum and the codes, so each row is read once.
+template <class T, int NU>
+__global__ void __launch_bounds__(256) kv_append_kernel(AppendArgs a) {
+  griddep_launch_dependents();
+  griddep_wait();
+  const bool is_v = blockIdx.z != 0;
+  AppendBlock b;
+  if (!append_block(a, is_v, &b)) return;
+  const int ulog = a.c.dim == 128 ? 3 : 2;  // units of a row: dim / 16
+  const int nr = is_v ? 0 : a.rope.rot / 8;  // rotated chunks
+  const bool inter = a.rope.interleaved != 0;
+  const T* src = static_cast<const T*>(is_v ? a.v : a.k) + (is_v ? a.v_head : a.k_head) * blockIdx.y;
+  const int64_t ts = is_v ? a.v_tok : a.k_tok;
+  float v[NU][16];
+  uint32_t am = 0;
+#pragma unroll
+  for (int k = 0; k < NU; ++k) {
+    const int e = threadIdx.x + k * blockDim.x, r = e >> ulog, u = e & ((1 << ulog) - 1);
+    const bool here = r < b.rows;
+    const bool pairs = !inter && u < nr / 2;  // chunks whose channels turn with one another's
+    const int ca = pairs ? u : 2 * u, cb = pairs ? u + nr / 2 : ca + 1;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) v[k][i] = 0.f;
+    if (here) {
+      const T* row = src + (b.row0 + r) * ts;
+      load8(row + ca * 8, v[k]);
+      load8(row + cb * 8, v[k] + 8);
+    }
+    const int p = !here ? 0 : a.pos ? a.pos[b.row0 + r] : b.pos0 + r;
+    if (here && pairs) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) append_turn(a.rope, p, ca * 8 + i, v[k][i], v[k][8 + i]);
+    } else if (here && inter && ca < nr) {  // neighbours; the second chunk's only if it turns too
+#pragma unroll
+      for (int i = 0; i < 4; ++i) append_turn(a.rope, p, ca * 4 + i, v[k][2 * i], v[k][2 * i + 1]);
+      if (cb < nr) {
+#pragma unroll
+        for (int i = 4; i < 8; ++i) append_turn(a.rope, p, ca * 4 + i, v[k][2 * i], v[k][2 * i + 1]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) am = max(am, __float_as_uint(v[k][i]) & 0x7fffffffu);
   }
+  const float inv = 1.f / append_scale(a, b, am);
+#pragma unroll
+  for (int k = 0; k < NU; ++k) {
+    const int e = threadIdx.x + k * blockDim.x, r = e >> ulog, u = e & ((1 << ulog) - 1);
+    const bool pairs = !inter && u < nr / 2;
+    const int ca = pairs ? u : 2 * u, cb = pairs ? u + nr / 2 : ca + 1;
+    if (r < b.rows) {
+      uint8_t* row = b.dst + (b.held + r) * a.c.tok_stride;
+      *reinterpret_cast<uint2*>(row + ca * 8) = encode8(v[k], inv, a.c.format);
+      *reinterpret_cast<uint2*>(row + cb * 8) = encode8(v[k] + 8, inv, a.c.format);
+    }
+  }
+}
+
+template <class T>
+int launch_append_t(const AppendArgs& a, cudaStream_t s) {
+  const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(a.q.n_tok) >> a.c.page_log2) + 2ll * a.q.n_seq),
+                  static_cast<unsigned>(a.c.Hkv), 2);
+  // 16-byte chunks: 8 channels (4 of fp32, loaded in twos)
+  uint64_t m = reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v);
+  m |= static_cast<uint64_t>(a.k_tok | a.k_head | a.v_tok | a.v_head) * sizeof(T);
+  const bool chunks = m % 16 == 0 && a.rope.rot % (a.rope.interleaved ? 8 : 16) == 0;
+  if (!chunks) return launch_k(kv_append_any_kernel<T>, grid, dim3(kAppendThreads), 0, s, a);
+  const int units = (a.c.dim / 16) << a.c.page_log2;  // of a full block: 64 .. 1024
+  if (units <= 256) return launch_k(kv_append_kernel<T, 1>, grid, dim3(static_cast<unsigned>(units)), 0, s, a);
+  if (units == 512) return launch_k(kv_append_kernel<T, 2>, grid, dim3(256), 0, s, a);
+  return launch_k(kv_append_kernel<T, 4>, grid, dim3(256), 0, s, a);
 }
 
 }  // namespace
 
 int launch_kv_append(const AppendArgs& a, cudaStream_t s) {
   if (a.q.n_tok == 0 || a.q.n_seq == 0) return 0;
-  const int64_t items = (static_cast<int64_t>(a.q.n_tok) >> a.c.page_log2) + 2ll * a.q.n_seq;
-  const dim3 grid(static_cast<unsigned>(items), static_cast<unsigned>(a.c.Hkv), 2);
   switch (a.dtype) {
-    case PCD_DTYPE_F32: return launch_k(kv_append_kernel<float>, grid, dim3(kAppendThreads), 0, s, a);
-    case PCD_DTYPE_BF16: return launch_k(kv_append_kernel<__nv_bfloat16>, grid, dim3(kAppendThreads), 0, s, a);
-    default: return launch_k(kv_append_kernel<__half>, grid, dim3(kAppendThreads), 0, s, a);
+    case PCD_DTYPE_F32: return launch_append_t<float>(a, s);
+    case PCD_DTYPE_BF16: return launch_append_t<__nv_bfloat16>(a, s);
+    default: return launch_append_t<__half>(a, s);
   }
 }
 

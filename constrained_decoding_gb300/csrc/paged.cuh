@@ -114,6 +114,40 @@ __device__ __forceinline__ float decode(uint8_t q, int format) {
   return __half2float(__half(__nv_cvt_fp8_to_halfraw(q, __NV_E4M3)));
 }
 
+// Eight values and their codes.
+template <class T>
+__device__ __forceinline__ void load8(const T* p, float* v) {
+  if constexpr (sizeof(T) == 4) {
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+  } else {
+    alignas(16) T x[8];
+    *reinterpret_cast<uint4*>(x) = *reinterpret_cast<const uint4*>(p);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = to_f(x[i]);
+  }
+}
+__device__ __forceinline__ uint2 encode8(const float* v, float inv, int format) {
+  uint32_t w[2];
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    w[j] = 0;
+    if (format == PCD_KV_INT8) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) w[j] |= static_cast<uint32_t>(encode(v[4 * j + i] * inv, PCD_KV_INT8)) << (8 * i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; i += 2) {
+        float x = v[4 * j + i] * inv, y = v[4 * j + i + 1] * inv;
+        if (x != x) x = 0.f;  // as encode()
+        if (y != y) y = 0.f;
+        w[j] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3)) << (8 * i);
+      }
+    }
+  }
+  return make_uint2(w[0], w[1]);
+}
+
 // Codes as fp16, exactly.  e4m3 by the conversion instruction (64 lanes a
 // clock on an SM, four times what masks and shifts reach); int8 with the sign
 // bit flipped as the low mantissa bits of 1024, minus 1152.

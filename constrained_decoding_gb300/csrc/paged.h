@@ -28,7 +28,7 @@ struct RopeKArgs {
   const int32_t* pos;  // per token, or nullptr: base + token
   int base;
 };
-int launch_rope(const RopeKArgs& a, cudaStream_t s);
+int launch_rope(const RopeKArgs& a, int sms, cudaStream_t s);
 
 // The cache: codes of (page, KV head, slot, channel), channels contiguous,
 // and one scale for each (page, KV head).

@@ -167,8 +167,9 @@ extern "C" int pcd_k_rope(const void* x, void* y, int dtype, int n_tok, int head
              "strides of y overlap rows");
   PCD_REFUSE(!rope_overlap_ok(x, y, es, n_tok, heads, head_dim, x_tok, x_head, y_tok, y_head), PCD_ERR_INVALID_ARG,
              "x and y overlap without being the same view");
-  PCD_REFUSE(static_cast<int64_t>(n_tok) * heads * head_dim >= (int64_t{1} << 38), PCD_ERR_INVALID_ARG, "too large");
-  return launched(pcd::launch_rope(a, static_cast<cudaStream_t>(stream)));
+  PCD_REFUSE(static_cast<int64_t>(n_tok) * head_dim >= (int64_t{1} << 31), PCD_ERR_INVALID_ARG,
+             "n_tok * head_dim is under 2^31");
+  return launched(pcd::launch_rope(a, device_sms(), static_cast<cudaStream_t>(stream)));
 }
 
 extern "C" int pcd_k_kv_append(const pcd_kv_pages* cache, const void* k, const void* v, int dtype, int64_t k_tok,
