@@ -4,18 +4,21 @@
 // A CTA owns 256 query rows of one sequence and KV head (rows are tokens x
 // the G query heads, flattened) as two tiles of 128 and walks key blocks of
 // 128:
-//   codes -> fp16, exactly     four warps, registers to swizzled shared memory
+//   codes to shared memory     bulk copies, one warp
+//   codes -> fp16, exactly     four warps, into 128-byte swizzled operand tiles
 //   S = Q K^T                  tcgen05.mma, 128 x 128, accumulator in TMEM
 //   w = exp2(S sk c + log2 sv - M + 8)   one thread a row
 //   O += w V8                  tcgen05.mma, w (fp16) from TMEM over S's columns
 //   l += w / sv                so out = O / l (see the rows kernel)
-// Each K and V block is converted once for both tiles; while one tile's rows
-// are in the softmax the tensor cores work for the other.  M moves, and O and l
-// are rescaled, only when a block exceeds it by 2^7.
+// Each K and V block is converted once for both tiles.  One thread issues all
+// MMAs in the order  P V of a tile, S of its next block, then the other tile:
+// while one tile's rows are in the softmax the tensor cores work for the
+// other.  M moves, and O and l are rescaled, only when a block exceeds it by
+// 2^7.
 //
 // Registers: 512 threads launch with 128 each; the two softmax warpgroups
-// hold a row of 128 scores and take 192, paid for by the converters (88) and
-// the issuers (40): 40 + 88 + 192 + 192 = 4 x 128.
+// hold a row of 128 scores and take 192, paid for by the other two (64 each):
+// 64 + 64 + 192 + 192 = 4 x 128.
 #include <algorithm>
 #include <cstdint>
 
@@ -42,7 +45,9 @@ struct TileCfg {
   static constexpr int kOp = kHalves * kHalf;           // one operand tile: 128 rows x D fp16
   static constexpr int kOffK = 2 * kOp;                 // after the two Q tiles
   static constexpr int kOffV = kOffK + 2 * kOp;
-  static constexpr int kOffSc = kOffV + 2 * kOp;        // [4][8] float4: constants of 16 keys
+  static constexpr int kRaw = kBlock * D;               // a block's K or V codes
+  static constexpr int kOffRaw = kOffV + 2 * kOp;       // K's, then V's
+  static constexpr int kOffSc = kOffRaw + 2 * kRaw;     // [4][8] float4: constants of 16 keys
   static constexpr int kOffBar = kOffSc + 4 * 8 * 16;
   static constexpr int kSmem = kOffBar + 256 + 1024;    // + alignment slack
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
@@ -72,6 +77,17 @@ __device__ __forceinline__ void tmem_st_16cols_async(uint32_t taddr, const uint3
       : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// Bulk copy of `bytes` (a multiple of 16, both addresses 16-byte aligned) to shared memory.
+__device__ __forceinline__ void bulk_g2s(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem_u32(dst)),
+               "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float m;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
+  return m;
+}
 template <int N>
 __device__ __forceinline__ void regs_up() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -99,8 +115,10 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
   uint64_t* p_full = bars + 10;  // [tile] weights in TMEM
   uint64_t* pv_done = bars + 12; // [tile] O current, S columns free
   uint64_t* q_full = bars + 14;  // [tile] Q rows staged
-  uint64_t* drain = bars + 16;   // [2] an issuer's MMAs are done
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 18);
+  uint64_t* raw_full = bars + 16;  // [K, V] codes landed, constants written
+  uint64_t* raw_free = bars + 18;  // [K, V] codes converted
+  uint64_t* drain = bars + 20;   // the issuer's MMAs are done
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 21);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   float4* sc = reinterpret_cast<float4*>(smem + C::kOffSc);
 
@@ -135,16 +153,18 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
-      mbar_init(&k_full[s], 128);
+      mbar_init(&k_full[s], 4);
       mbar_init(&k_free[s], 1);
-      mbar_init(&v_full[s], 128);
+      mbar_init(&v_full[s], 4);
       mbar_init(&v_free[s], 1);
       mbar_init(&s_full[s], 2);
-      mbar_init(&p_full[s], 128);
+      mbar_init(&p_full[s], 4);
       mbar_init(&pv_done[s], 1);
-      mbar_init(&q_full[s], 128);
-      mbar_init(&drain[s], 1);
+      mbar_init(&q_full[s], 4);
+      mbar_init(&raw_full[s], 1);
+      mbar_init(&raw_free[s], 4);
     }
+    mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -163,134 +183,169 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
     *abort_flag = 1;
   };
 
+  const int last_page = (len - 1) >> a.c.page_log2;
+  int raw_issued = 0;  // blocks whose K (and V) copies were issued, by the copying warp
+
   if (warp < 4) {
-    // ------------------------------------------------------------ MMA issuers
-    regs_down<40>();
-    if (warp < 2 && lane == 0 && nb > 0) {
-      const bool is_s = warp == 0;
+    regs_down<64>();
+    if (warp == 0 && lane == 0 && nb > 0) {
+      // ------------------------------------------------------------ MMA issuer
       constexpr uint32_t kIdS = idesc_f16_f32(kTile, kBlock);
       constexpr uint32_t kIdO = idesc_f16_f32(kTile, D) | (1u << 16);  // B (V) is MN-major
-      bool ok = true;
+      const int nt = two ? 2 : 1;
+      auto issue_s = [&](int t, int st) {
+        tc_fence_after_sync();
+        const uint32_t qa = smem_u32(smem + t * C::kOp), ka = smem_u32(smem + C::kOffK + st * C::kOp);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t o = (k >> 2) * kHalf + (k & 3) * 32;
+          umma_f16(tbase + t * kBlock, sdesc_kmajor_sw128(qa + o), sdesc_kmajor_sw128(ka + o), kIdS, k > 0 ? 1u : 0u);
+        }
+        umma_commit(&s_full[t]);
+        mbar_arrive(&s_full[t]);  // orders the constants, which the commit alone would not
+        if (t == nt - 1) umma_commit(&k_free[st]);
+      };
+      bool ok = mbar_wait(&k_full[0], 0, kWaitNs);
+      for (int t = 0; ok && t < nt; ++t) {
+        ok = mbar_wait(&q_full[t], 0, kWaitNs);
+        if (ok) issue_s(t, 0);
+      }
       for (int i = 0; ok && i < nb; ++i) {
-        const int st = i & 1;
-        const uint32_t par = static_cast<uint32_t>((i >> 1) & 1);
-        ok = mbar_wait(is_s ? &k_full[st] : &v_full[st], par, kWaitNs);
-        for (int t = 0; ok && t < (two ? 2 : 1); ++t) {
-          if (is_s) {
-            if (i == 0) ok = mbar_wait(&q_full[t], 0, kWaitNs);
-            else ok = mbar_wait(&pv_done[t], static_cast<uint32_t>((i - 1) & 1), kWaitNs);
-            if (!ok) break;
-            tc_fence_after_sync();
-            const uint32_t qa = smem_u32(smem + t * C::kOp), ka = smem_u32(smem + C::kOffK + st * C::kOp);
+        const int st = i & 1, sn = st ^ 1;
+        for (int t = 0; ok && t < nt; ++t) {
+          if (t == 0) ok = mbar_wait(&v_full[st], static_cast<uint32_t>((i >> 1) & 1), kWaitNs);
+          ok = ok && mbar_wait(&p_full[t], static_cast<uint32_t>(i & 1), kWaitNs);
+          if (!ok) break;
+          tc_fence_after_sync();
+          const uint32_t va = smem_u32(smem + C::kOffV + st * C::kOp);
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-              const uint32_t o = (k >> 2) * kHalf + (k & 3) * 32;
-              umma_f16(tbase + t * kBlock, sdesc_kmajor_sw128(qa + o), sdesc_kmajor_sw128(ka + o), kIdS, k > 0 ? 1u : 0u);
-            }
-            umma_commit(&s_full[t]);
-            mbar_arrive(&s_full[t]);
-          } else {
-            ok = mbar_wait(&p_full[t], static_cast<uint32_t>(i & 1), kWaitNs);
-            if (!ok) break;
-            tc_fence_after_sync();
-            const uint32_t va = smem_u32(smem + C::kOffV + st * C::kOp);
-#pragma unroll
-            for (int k = 0; k < kBlock / 16; ++k)
-              umma_f16_ts(tbase + col_o + t * D, tbase + t * kBlock + k * 8,
-                          sdesc_mnmajor_sw128(va + k * 16 * 128, kHalf, 1024), kIdO, (i > 0 || k > 0) ? 1u : 0u);
-            umma_commit(&pv_done[t]);
+          for (int k = 0; k < kBlock / 16; ++k)
+            umma_f16_ts(tbase + col_o + t * D, tbase + t * kBlock + k * 8,
+                        sdesc_mnmajor_sw128(va + k * 16 * 128, kHalf, 1024), kIdO, (i > 0 || k > 0) ? 1u : 0u);
+          umma_commit(&pv_done[t]);
+          if (t == nt - 1) umma_commit(&v_free[st]);
+          if (i + 1 < nb) {
+            if (t == 0) ok = mbar_wait(&k_full[sn], static_cast<uint32_t>(((i + 1) >> 1) & 1), kWaitNs);
+            // S takes the columns that P V reads its weights from
+            ok = ok && mbar_wait(&pv_done[t], static_cast<uint32_t>(i & 1), kWaitNs);
+            if (ok) issue_s(t, sn);
           }
         }
-        if (ok) umma_commit(is_s ? &k_free[st] : &v_free[st]);
         if (*abort_flag) ok = false;
       }
       if (!ok) fail(DEV_WAIT_TIMEOUT_MMA);
-      umma_commit(&drain[warp]);  // every MMA of this thread ends before TMEM is released
-      if (!mbar_wait(&drain[warp], 0, kDrainWaitNs)) record_error(a.err, DEV_WAIT_TIMEOUT_DRAIN);
+      umma_commit(drain);  // every MMA ends before TMEM is released
+      if (!mbar_wait(drain, 0, kDrainWaitNs)) record_error(a.err, DEV_WAIT_TIMEOUT_DRAIN);
+    } else if (warp == 1 && nb > 0) {
+      // ------------------------------------------------------------ copies of codes, constants of keys
+      const int32_t* tab = a.q.table + static_cast<int64_t>(it.seq) * a.q.table_stride;
+      const int page = 1 << a.c.page_log2, npg = kBlock >> a.c.page_log2;
+      const bool rows_together = a.c.tok_stride == D;
+      auto fetch = [&](int b) {  // the page of lane l of block b
+        const int pg = (b << 7 >> a.c.page_log2) + lane;
+        return lane < npg && pg <= last_page ? tab[pg] : -1;
+      };
+      int id_next = fetch(b0);
+      bool ok = true;
+      for (int i = 0; i < nb && ok; ++i) {
+        const int id = id_next, j0 = (b0 + i) * kBlock;
+        if (i + 1 < nb) id_next = fetch(b0 + i + 1);
+        const bool good = id >= 0 && id < a.c.n_pages;
+        if (lane < npg && j0 + lane * page < len && !good) record_error(a.err, DEV_BAD_INDEX);
+        const int rows = good ? min(page, len - j0 - lane * page) : 0;
+        const uint32_t total = __reduce_add_sync(0xffffffffu, static_cast<unsigned>(rows) * D);
+        const int64_t off = (good ? id : 0) * a.c.page_stride + hk * a.c.head_stride;
+#pragma unroll 1
+        for (int kv = 0; kv < 2 && ok; ++kv) {
+          if (i > 0) ok = mbar_wait(&raw_free[kv], static_cast<uint32_t>((i - 1) & 1), kWaitNs);
+          ok = __all_sync(0xffffffffu, ok && !*abort_flag);
+          if (!ok) break;
+          const uint8_t* base = kv ? a.c.v : a.c.k;
+          uint8_t* raw = smem + C::kOffRaw + kv * C::kRaw;
+          if (kv == 0) {
+            // 16 keys to a lane: K scale, log2 and reciprocal of the V scale, seen or not
+            const int pl = lane * 16 >> a.c.page_log2;
+            const int cid = __shfl_sync(0xffffffffu, good ? id : -1, pl & 31);
+            if (lane < kBlock / 16) {
+              float4 c = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (cid >= 0 && j0 + lane * 16 < len) {
+                float v = a.c.vs[static_cast<int64_t>(cid) * a.c.Hkv + hk];
+                if (v < kScaleFloor) v = kScaleFloor;  // a NaN stays
+                c = make_float4(a.c.ks[static_cast<int64_t>(cid) * a.c.Hkv + hk], lg2(v), 1.f / v, 1.f);
+              }
+              sc[(i & 3) * 8 + lane] = c;  // block i - 4 left the softmax before V of block i - 2 was converted
+            }
+            __syncwarp();
+          }
+          if (lane == 0) mbar_arrive_expect_tx(&raw_full[kv], total);
+          __syncwarp();
+          if (rows_together) {
+            if (rows > 0) bulk_g2s(raw + lane * page * D, base + off, rows * D, &raw_full[kv]);
+          } else {
+            for (int p = 0; p < npg; ++p) {
+              const int n = __shfl_sync(0xffffffffu, rows, p);
+              const int64_t o = __shfl_sync(0xffffffffu, off, p);
+              for (int r = lane; r < n; r += 32)
+                bulk_g2s(raw + (p * page + r) * D, base + o + r * a.c.tok_stride, D, &raw_full[kv]);
+            }
+          }
+          raw_issued = 2 * i + kv + 1;
+        }
+      }
+      if (!ok && lane == 0) fail(DEV_WAIT_TIMEOUT_PRODUCER);
     }
     __syncwarp();
   } else if (warp < 8) {
     // ------------------------------------------------------------ codes -> fp16
-    // Thread -> rows (tid / 4 mod 8) + 8 j, chunk (tid mod 4): eight rows of one chunk make a store phase.
-    regs_down<88>();
-    const int tid = threadIdx.x - 128;
-    constexpr int kCh = D / 16;             // 16-code chunks of a row
-    constexpr int kPer = kBlock * kCh / 128;  // chunks of a thread: 8 or 4
-    const int32_t* tab = a.q.table + static_cast<int64_t>(it.seq) * a.q.table_stride;
-    const int last_page = (len - 1) >> a.c.page_log2;
-    auto where = [&](int j, int* row, int* ch) {  // chunk j of this thread
-      const int x = j * 128 + tid;
-      *row = ((x >> 5) / (kCh / 4)) * 8 + ((x >> 2) & 7);
-      *ch = ((x >> 5) % (kCh / 4)) * 4 + (x & 3);
-    };
-    auto load = [&](const uint8_t* base, int b, uint4* v) {
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        int row, ch;
-        where(j, &row, &ch);
-        const int key = b * kBlock + row;
-        const int pg = key >> a.c.page_log2;
-        const int id = key < len ? tab[pg] : -1;  // slots behind the last token read as zeros, whatever they hold
-        v[j] = make_uint4(0u, 0u, 0u, 0u);
-        if (id >= 0 && id < a.c.n_pages)
-          v[j] = *reinterpret_cast<const uint4*>(base + id * a.c.page_stride + hk * a.c.head_stride +
-                                                 (key & ((1 << a.c.page_log2) - 1)) * a.c.tok_stride + ch * 16);
-      }
-    };
-    auto store = [&](uint8_t* dst, const uint4* v) {
-#pragma unroll
-      for (int j = 0; j < kPer; ++j) {
-        int row, ch;
-        where(j, &row, &ch);
-        const uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
-        uint32_t h[8];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) codes4_half<FMT>(w[x], &h[2 * x], &h[2 * x + 1]);
-        uint8_t* p = dst + (ch >> 2) * kHalf;
-        const int c8 = (ch & 3) * 2;
-        *reinterpret_cast<uint4*>(p + swz128(row, c8)) = make_uint4(h[0], h[1], h[2], h[3]);
-        *reinterpret_cast<uint4*>(p + swz128(row, c8 + 1)) = make_uint4(h[4], h[5], h[6], h[7]);
-      }
-    };
-    // constants of 16 keys: K scale, log2 and reciprocal of the V scale, seen or not
-    auto constants = [&](int i) {
-      if (tid < kBlock / 16) {
-        const int pg = ((b0 + i) * kBlock + tid * 16) >> a.c.page_log2;
-        float4 c = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (pg <= last_page) {
-          const int id = tab[pg];
-          if (id >= 0 && id < a.c.n_pages) {
-            float v = a.c.vs[static_cast<int64_t>(id) * a.c.Hkv + hk];
-            if (v < kScaleFloor) v = kScaleFloor;  // a NaN stays
-            c = make_float4(a.c.ks[static_cast<int64_t>(id) * a.c.Hkv + hk], lg2(v), 1.f / v, 1.f);
-          } else {
-            record_error(a.err, DEV_BAD_INDEX);
-          }
-        }
-        sc[(i & 3) * 8 + tid] = c;
-      }
-    };
-    uint4 kv[kPer], vv[kPer];
+    // Eight lanes read 128 bytes of a row pair and write 8 different 16-byte
+    // places of the swizzled rows: at D 128 lanes 0-3 take the first half of one
+    // row and lanes 4-7 the second half of the other, whose XOR differs in its last bit.
+    regs_down<64>();
+    const int tid = threadIdx.x - 128, q8 = lane & 7, ph = lane >> 3;
+    constexpr int kPer = kBlock * D / 16 / 128;  // 16-code chunks of a thread: 8 or 4
+    constexpr int kStep = kBlock / kPer;         // rows between them
+    const int row0 = D == 128 ? (((tid >> 5) * 2 + (ph >> 1)) * 2 + ((q8 >> 2) ^ (ph & 1))) : ((tid >> 3) * 2 + (q8 >> 2));
+    const int ch = D == 128 ? q8 : (q8 & 3);
+    const uint8_t* raw0 = smem + C::kOffRaw + row0 * D + ch * 16;
+    const uint32_t dst0 = (ch >> 2) * kHalf + swz128(row0, (ch & 3) * 2), dst1 = (ch >> 2) * kHalf + swz128(row0, (ch & 3) * 2 + 1);
     bool ok = true;
-    if (nb > 0) load(a.c.k, b0, kv);
-    for (int i = 0; i < nb; ++i) {
+    for (int i = 0; i < nb && ok; ++i) {
       const int st = i & 1;
-      const uint32_t par = static_cast<uint32_t>(((i - 2) >> 1) & 1);
-      load(a.c.v, b0 + i, vv);
-      if (i >= 2) ok = mbar_wait(&k_free[st], par, kWaitNs);
-      ok = __all_sync(0xffffffffu, ok && !*abort_flag);
-      if (!ok) break;
-      constants(i);  // slot i mod 4: block i - 4 left the softmax before v_free of block i - 3
-      store(smem + C::kOffK + st * C::kOp, kv);
-      fence_proxy_async_smem();
-      mbar_arrive(&k_full[st]);
-      if (i + 1 < nb) load(a.c.k, b0 + i + 1, kv);
-      if (i >= 2) ok = mbar_wait(&v_free[st], par, kWaitNs);
-      ok = __all_sync(0xffffffffu, ok && !*abort_flag);
-      if (!ok) break;
-      store(smem + C::kOffV + st * C::kOp, vv);
-      fence_proxy_async_smem();
-      mbar_arrive(&v_full[st]);
+      const int live = min(kBlock, len - (b0 + i) * kBlock);  // rows behind the last token read as zeros
+#pragma unroll 1
+      for (int kv = 0; kv < 2; ++kv) {
+        ok = mbar_wait(&raw_full[kv], static_cast<uint32_t>(i & 1), kWaitNs);
+        if (ok && i >= 2) ok = mbar_wait(kv ? &v_free[st] : &k_free[st], static_cast<uint32_t>(((i - 2) >> 1) & 1), kWaitNs);
+        ok = __all_sync(0xffffffffu, ok && !*abort_flag);
+        if (!ok) break;
+        bool whole = live == kBlock;
+#pragma unroll
+        for (int g = 0; g < 8; ++g) whole = whole && sc[(i & 3) * 8 + g].w != 0.f;
+        const uint8_t* src = raw0 + kv * C::kRaw;
+        uint8_t* dst = smem + (kv ? C::kOffV : C::kOffK) + st * C::kOp;
+#pragma unroll
+        for (int j = 0; j < kPer; ++j) {
+          uint4 v = *reinterpret_cast<const uint4*>(src + j * kStep * D);
+          if (!whole) {
+            const int row = row0 + j * kStep;
+            if (row >= live || sc[(i & 3) * 8 + (row >> 4)].w == 0.f) v = make_uint4(0u, 0u, 0u, 0u);
+          }
+          uint32_t h[8];
+          codes4_half<FMT>(v.x, &h[0], &h[1]);
+          codes4_half<FMT>(v.y, &h[2], &h[3]);
+          codes4_half<FMT>(v.z, &h[4], &h[5]);
+          codes4_half<FMT>(v.w, &h[6], &h[7]);
+          // kStep is a multiple of 8: the swizzle of row0 holds for its other rows
+          *reinterpret_cast<uint4*>(dst + dst0 + j * kStep * 128) = make_uint4(h[0], h[1], h[2], h[3]);
+          *reinterpret_cast<uint4*>(dst + dst1 + j * kStep * 128) = make_uint4(h[4], h[5], h[6], h[7]);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(kv ? &v_full[st] : &k_full[st]);
+          mbar_arrive(&raw_free[kv]);
+        }
+      }
     }
     if (!ok && lane == 0) fail(DEV_WAIT_TIMEOUT_PRODUCER);
   } else {
@@ -344,7 +399,8 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
         *reinterpret_cast<uint4*>(q + (c >> 3) * kHalf + swz128(rt, c & 7)) = make_uint4(w[0], w[1], w[2], w[3]);
       }
       fence_proxy_async_smem();
-      mbar_arrive(&q_full[t]);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&q_full[t]);
       const int wmin = __reduce_min_sync(0xffffffffu, vis);  // keys that every row of the warp sees
       for (int i = 0; i < nb; ++i) {
         ok = __all_sync(0xffffffffu, mbar_wait(&s_full[t], static_cast<uint32_t>(i & 1), kWaitNs) && !*abort_flag);
@@ -362,10 +418,14 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
         for (int g = 0; g < 8; ++g) {
           const float4 k = cs[g];
           plain = plain && k.w != 0.f;
-          float m = s[16 * g];
+          float m = max3(s[16 * g], s[16 * g + 1], s[16 * g + 2]), m1 = max3(s[16 * g + 3], s[16 * g + 4], s[16 * g + 5]);
 #pragma unroll
-          for (int e = 1; e < 16; ++e) m = fmaxf(m, s[16 * g + e]);
-          mx = fmaxf(mx, fmaf(m, qs * k.x, k.y));
+          for (int e = 6; e < 14; e += 4) {
+            m = max3(m, s[16 * g + e], s[16 * g + e + 1]);
+            m1 = max3(m1, s[16 * g + e + 2], s[16 * g + e + 3]);
+          }
+          m = max3(m, s[16 * g + 14], s[16 * g + 15]);
+          mx = fmaxf(mx, fmaf(fmaxf(m, m1), qs * k.x, k.y));
         }
         if (!plain) {
           // some key of the block is hidden from some row: x in place of S, -inf where hidden
@@ -416,23 +476,25 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
           for (int g = 2 * q2; g < 2 * q2 + 2; ++g) {
             const float4 k = cs[g];
             const float ak = plain ? qs * k.x : 1.f, bk = (plain ? k.y : 0.f) - mb;
-            float l0 = 0.f, l1 = 0.f;
+            const float2 a2 = make_float2(ak, ak), b2 = make_float2(bk, bk);
+            float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
             for (int e = 0; e < 16; e += 2) {
-              const float p0 = ex2_approx(fmaf(s[16 * g + e], ak, bk));
-              const float p1 = ex2_approx(fmaf(s[16 * g + e + 1], ak, bk));
-              l0 += p0;
-              l1 += p1;
-              w[(g & 1) * 8 + e / 2] = pack2(p0, p1);
+              float2 p = __ffma2_rn(make_float2(s[16 * g + e], s[16 * g + e + 1]), a2, b2);
+              p.x = ex2_approx(p.x);
+              p.y = ex2_approx(p.y);
+              sum = __fadd2_rn(sum, p);
+              w[(g & 1) * 8 + e / 2] = pack2(p.x, p.y);
             }
             // a poisoned scale (NaN) counts only for rows that see its keys
-            l = fmaf(l0 + l1, plain || vis > j0 + 16 * g ? k.z : 0.f, l);
+            l = fmaf(sum.x + sum.y, plain || vis > j0 + 16 * g ? k.z : 0.f, l);
           }
           tmem_st_16cols_async(ts + 16 * q2, w);
         }
         tmem_st_wait();
         tc_fence_before_sync();
-        mbar_arrive(&p_full[t]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[t]);
       }
       if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[t], static_cast<uint32_t>((nb - 1) & 1), kWaitNs) && !*abort_flag);
       if (!ok && lane == 0) fail(DEV_WAIT_TIMEOUT_EPILOGUE);
@@ -485,7 +547,13 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
   }
   tc_fence_before_sync();
   __syncthreads();
+  if (warp == 1) {  // nothing of this CTA's copies may still be landing when it exits
+    const int k = (raw_issued + 1) / 2, v = raw_issued / 2;
+    if (k > 0) mbar_wait(&raw_full[0], static_cast<uint32_t>((k - 1) & 1), kDrainWaitNs);
+    if (v > 0) mbar_wait(&raw_full[1], static_cast<uint32_t>((v - 1) & 1), kDrainWaitNs);
+  }
   if (warp == 0) {
+    __syncwarp();
     tc_fence_after_sync();
     tmem_dealloc(tbase, 512);
   }
