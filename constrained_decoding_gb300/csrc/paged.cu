@@ -178,7 +178,7 @@ __device__ __forceinline__ bool append_block(const AppendArgs& a, bool is_v, App
   // item -> (sequence, page of its new range)
   const SeqItem it = find_item(a.q, static_cast<int>(blockIdx.x), 1, a.c.page_log2, 2);
   if (it.seq < 0) return false;
-  const int n = it.n, len = a.q.kv_len[it.seq];
+  const int n = it.n, len = it.len;
   if (n == 0) return false;
   if (n < 0 || it.row0 < 0 || n > a.q.n_tok - it.row0 || len < n || len > kMaxLen ||
       len > static_cast<int64_t>(a.q.table_stride) << a.c.page_log2) {
@@ -395,25 +395,24 @@ struct RowsCfg {
 struct RowsSeq {
   int row0, n, len, tiles, blocks;  // tiles of 16 rows (0: nothing to do), 16-key blocks of an item
 };
-__device__ __forceinline__ RowsSeq rows_seq(const PagedAttnArgs& a, int s) {
-  RowsSeq q;
-  q.row0 = a.q.q_off[s];
-  q.n = a.q.q_off[s + 1] - q.row0;
-  q.len = a.q.kv_len[s];
-  q.tiles = 0;
-  if (q.n != 0) {
-    if (q.n < 0 || q.row0 < 0 || q.n > a.q.n_tok - q.row0) {
-      record_error(a.err, DEV_BAD_INDEX);
-    } else {
-      q.tiles = (q.n * a.G + 15) >> 4;
-      if (q.len < 0 || q.len > kMaxLen || q.len > static_cast<int64_t>(a.q.table_stride) << a.c.page_log2) {
-        record_error(a.err, DEV_BAD_INDEX);
-        q.len = 0;
-      }
-    }
+__device__ __forceinline__ RowsSeq rows_seq(const PagedAttnArgs& a, int row0, int n, int len) {
+  RowsSeq q{row0, n, len, 0, 1};
+  if (n == 0) return q;
+  if (n < 0 || row0 < 0 || n > a.q.n_tok - row0) {
+    record_error(a.err, DEV_BAD_INDEX);
+    return q;
+  }
+  q.tiles = (n * a.G + 15) >> 4;
+  if (len < 0 || len > kMaxLen || len > static_cast<int64_t>(a.q.table_stride) << a.c.page_log2) {
+    record_error(a.err, DEV_BAD_INDEX);
+    q.len = 0;
   }
   q.blocks = max(1, (q.len + 15) >> 4);  // an item without keys still writes its rows
   return q;
+}
+__device__ __forceinline__ RowsSeq rows_seq(const PagedAttnArgs& a, int s) {
+  const int row0 = a.q.q_off[s];
+  return rows_seq(a, row0, static_cast<int>(static_cast<unsigned>(a.q.q_off[s + 1]) - static_cast<unsigned>(row0)), a.q.kv_len[s]);
 }
 __device__ __forceinline__ int64_t rows_units(const PagedAttnArgs& a, const RowsSeq& q) {
   return static_cast<int64_t>(q.tiles) * a.c.Hkv * q.blocks;
@@ -469,7 +468,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) paged_attn_rows_kernel(PagedAt
     if (it.seq < 0) return;
     seq = it.seq;
     tile = it.local;
-    sq = rows_seq(a, seq);
+    sq = rows_seq(a, it.row0, it.n, it.len);
     if (tile >= sq.tiles) return;
   }
   for (;;) {

@@ -58,31 +58,45 @@ struct KernelSetup {
 // ------------------------------------------------------------------ sequences
 constexpr int kMaxLen = 0x7ffffc00;  // tokens of a sequence: positions and their roundings stay in 32 bits
 struct SeqItem {
-  int seq, local, row0, n;  // sequence (-1: none), item within it, its first row and its rows
+  int seq, local, row0, n, len;  // sequence (-1: none), item within it, its first row, its rows, its cached tokens
 };
 // The sequence of work item `idx` when sequence s owns the items
 // [f(s), f(s + 1)), f(s) = (q_off[s] * mul >> shift) + add * s: a bound on its
-// tiles that needs no prefix sum.  A warp narrows 32 ways at a time.
+// tiles that needs no prefix sum.  A warp narrows 32 ways at a time; lanes
+// fetch all that a sequence has at once, so up to 32 sequences cost one trip
+// to memory.
 __device__ __forceinline__ SeqItem find_item(const SeqView& q, int idx, int mul, int shift, int add) {
   const int lane = threadIdx.x & 31;
-  auto f = [&](int s) {
-    return static_cast<int>(static_cast<unsigned>(q.q_off[s]) * static_cast<unsigned>(mul) >> shift) + add * s;
+  auto f = [&](int off, int s) {
+    return static_cast<int>(static_cast<unsigned>(off) * static_cast<unsigned>(mul) >> shift) + add * s;
   };
   int lo = 0, hi = q.n_seq;
-  do {
+  while (true) {
     const int step = (hi - lo + 31) >> 5;
     const int s = lo + lane * step;
-    const unsigned b = __ballot_sync(0xffffffffu, s < hi && f(s) <= idx);
-    if (b == 0) return SeqItem{-1, 0, 0, 0};
-    lo += (31 - __clz(b)) * step;
+    int off = 0, end = 0, len = 0;
+    if (s < hi) {
+      off = q.q_off[s];
+      if (step == 1) {
+        end = q.q_off[s + 1];
+        len = q.kv_len[s];
+      }
+    }
+    const unsigned b = __ballot_sync(0xffffffffu, s < hi && f(off, s) <= idx);
+    if (b == 0) return SeqItem{-1, 0, 0, 0, 0};
+    const int l = 31 - __clz(b);
+    if (step == 1) {
+      SeqItem it;
+      it.seq = lo + l;
+      it.row0 = __shfl_sync(0xffffffffu, off, l);
+      it.n = static_cast<int>(static_cast<unsigned>(__shfl_sync(0xffffffffu, end, l)) - static_cast<unsigned>(it.row0));
+      it.len = __shfl_sync(0xffffffffu, len, l);
+      it.local = idx - f(it.row0, it.seq);
+      return it;
+    }
+    lo += l * step;
     hi = min(hi, lo + step);
-  } while (hi - lo > 1);
-  SeqItem it;
-  it.seq = lo;
-  it.local = idx - f(lo);
-  it.row0 = q.q_off[lo];
-  it.n = q.q_off[lo + 1] - it.row0;
-  return it;
+  }
 }
 
 // ---------------------------------------------------------------------- codes

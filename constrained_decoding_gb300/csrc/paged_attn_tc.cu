@@ -126,21 +126,21 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
   const int hk = blockIdx.y, z = blockIdx.z;
   griddep_launch_dependents();
   griddep_wait();
-  // the last rows of a causal prompt see the most keys: they start first
-  const SeqItem it = find_item(a.q, static_cast<int>(gridDim.x - 1 - blockIdx.x), a.G, 8, 1);
+  const SeqItem it = find_item(a.q, static_cast<int>(blockIdx.x), a.G, 8, 1);
   if (it.seq < 0 || it.n == 0) return;
   if (it.n < 0 || it.row0 < 0 || it.n > a.q.n_tok - it.row0) {
     if (threadIdx.x == 0) record_error(a.err, DEV_BAD_INDEX);
     return;
   }
   const int R = it.n * a.G;
-  if (it.local >= (R + kRowsCta - 1) / kRowsCta) return;
-  int len = a.q.kv_len[it.seq];
+  const int tiles = (R + kRowsCta - 1) / kRowsCta;
+  if (it.local >= tiles) return;
+  int len = it.len;
   if (len < 0 || len > kMaxLen || len > static_cast<int64_t>(a.q.table_stride) << a.c.page_log2) {
     if (threadIdx.x == 0) record_error(a.err, DEV_BAD_INDEX);
     len = 0;
   }
-  const int r0 = it.local * kRowsCta;
+  const int r0 = (tiles - 1 - it.local) * kRowsCta;  // the last rows of a causal prompt see the most keys: they start first
   const int r_end = min(r0 + kRowsCta, R);
   const bool two = r_end - r0 > kTile;
   const int first = a.causal ? len - it.n + 1 : len;
