@@ -364,40 +364,53 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
     float m_ref = -INFINITY, l = 0.f, qs = 0.f;
     bool ok = active;
     if (active && nb > 0) {
-      // ---- this row of Q, as fp16 (bf16 rows scaled by a power of two)
-      const T* src = static_cast<const T*>(a.x) + tok * a.x_tok + hq * a.x_head;
-      const bool wide = (reinterpret_cast<uintptr_t>(src) & 15) == 0;
-      auto eight = [&](int c, T* v) {
-        if (wide) {
-          *reinterpret_cast<uint4*>(v) = *reinterpret_cast<const uint4*>(src + 8 * c);
+      // ---- the warp's 32 rows of Q, as fp16 (bf16 rows scaled by a power of two): D / 8 lanes to a row,
+      // every load in flight at once
+      constexpr int kLanes = D / 8, kAt = 32 / kLanes;  // rows of one load
+      const int64_t mine = tok * a.x_tok + hq * a.x_head;
+      const int c = lane % kLanes;
+      alignas(16) T v[32 / kAt][8];
+#pragma unroll
+      for (int j = 0; j < 32 / kAt; ++j) {
+        const int r32 = j * kAt + lane / kLanes;
+        const T* src = static_cast<const T*>(a.x) + __shfl_sync(0xffffffffu, mine, r32) + 8 * c;
+        if (((reinterpret_cast<uintptr_t>(a.x) | static_cast<uint64_t>(a.x_tok | a.x_head) * 2) & 15) == 0) {
+          *reinterpret_cast<uint4*>(v[j]) = *reinterpret_cast<const uint4*>(src);
         } else {
 #pragma unroll
-          for (int x = 0; x < 8; ++x) v[x] = src[8 * c + x];
-        }
-      };
-      uint32_t am = 0;
-      if (!std::is_same<T, __half>::value) {
-#pragma unroll 4
-        for (int c = 0; c < D / 8; ++c) {
-          alignas(16) T v[8];
-          eight(c, v);
-#pragma unroll
-          for (int x = 0; x < 8; ++x) am = max(am, __float_as_uint(to_f(v[x])) & 0x7fffffffu);
+          for (int x = 0; x < 8; ++x) v[j][x] = src[x];
         }
       }
-      float down;
-      qs = row_power<T>(am, &down) * a.scale_log2;
-      uint8_t* q = smem + t * C::kOp;
-#pragma unroll 4
-      for (int c = 0; c < D / 8; ++c) {
-        alignas(16) T v[8];
-        eight(c, v);
+      uint8_t* q = smem + t * C::kOp + (c >> 3) * kHalf;
+      qs = 1.f;
+#pragma unroll
+      for (int j = 0; j < 32 / kAt; ++j) {
+        const int r32 = j * kAt + lane / kLanes, row = 32 * (warp & 3) + r32;
         uint32_t w[4];
+        if (std::is_same<T, __half>::value) {
 #pragma unroll
-        for (int x = 0; x < 4; ++x)
-          w[x] = valid ? pack2(to_f(v[2 * x]) * down, to_f(v[2 * x + 1]) * down) : 0u;
-        *reinterpret_cast<uint4*>(q + (c >> 3) * kHalf + swz128(rt, c & 7)) = make_uint4(w[0], w[1], w[2], w[3]);
+          for (int x = 0; x < 4; ++x) w[x] = reinterpret_cast<const uint32_t*>(v[j])[x];
+        } else {
+          uint32_t am = 0;
+#pragma unroll
+          for (int x = 0; x < 8; ++x) am = max(am, __float_as_uint(to_f(v[j][x])) & 0x7fffffffu);
+#pragma unroll
+          for (int o = kLanes / 2; o > 0; o >>= 1) am = max(am, __shfl_xor_sync(0xffffffffu, am, o));
+          float down;
+          const float up = row_power<T>(am, &down);
+#pragma unroll
+          for (int o = 0; o < kAt; ++o) {
+            const float u = __shfl_sync(0xffffffffu, up, o * kLanes);
+            if (lane == j * kAt + o) qs = u;
+          }
+#pragma unroll
+          for (int x = 0; x < 4; ++x) w[x] = pack2(to_f(v[j][2 * x]) * down, to_f(v[j][2 * x + 1]) * down);
+        }
+        const bool in = r0 + t * kTile + row < r_end;  // rows behind the last are zeros
+        *reinterpret_cast<uint4*>(q + swz128(row, c & 7)) =
+            in ? make_uint4(w[0], w[1], w[2], w[3]) : make_uint4(0u, 0u, 0u, 0u);
       }
+      qs *= a.scale_log2;
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full[t]);
@@ -504,35 +517,64 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
     const bool have = ok && nb > 0;
     const bool split = a.plan.n_splits > 1;
     const int64_t prow = (static_cast<int64_t>(z) * a.q.n_tok + tok) * a.Hq + hq;
-    T* out = static_cast<T*>(a.out) + tok * a.out_tok + hq * a.out_head;
     const float il = l == 0.f ? 0.f : 1.f / l;
     if (active) {
+      // The warp turns its rows through its part of the Q tile (every S is done), 256 bytes of a row at a
+      // time, so that 16 lanes write them side by side.
+      uint8_t* turn = smem + t * C::kOp + (warp & 3) * (C::kOp / 4);
+      constexpr int kRowB = D == 128 ? 256 : 128;             // bytes of a row in a pass: the tile's share
+      constexpr int kChunks = kRowB / 16;
+      const int passes = D * (split ? 4 : 2) / kRowB;
+      const int64_t mine = split ? prow * D : tok * a.out_tok + hq * a.out_head;
+      const uint32_t kept = __ballot_sync(0xffffffffu, valid && (!split || (have && l != 0.f)));
+      const bool wide =
+          split || ((reinterpret_cast<uintptr_t>(a.out) | static_cast<uint64_t>(a.out_tok | a.out_head) * 2) & 15) == 0;
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
-        float o[32];
-        if (have) {
-          tmem_ld_32cols_async(to + 32 * c, o);
-          tmem_ld_wait();
-        }
-        __syncwarp();
-        if (valid && split && have && l != 0.f) {
-#pragma unroll
-          for (int x = 0; x < 8; ++x)
-            *reinterpret_cast<float4*>(a.part_o + prow * D + 32 * c + 4 * x) =
-                make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
-        } else if (valid && !split) {
+      for (int p = 0; p < passes; ++p) {
+        // this thread's row: kRowB bytes from column p * (kRowB / element)
+#pragma unroll 1
+        for (int c = 0; c < (split ? kRowB / 4 : kRowB / 2) / 32; ++c) {
+          float o[32];
+          const int d = p * (split ? kRowB / 4 : kRowB / 2) + 32 * c;
+          if (have) {
+            tmem_ld_32cols_async(to + d, o);
+            tmem_ld_wait();
+          }
           const bool some = have && l != 0.f;
-          if ((reinterpret_cast<uintptr_t>(out) & 15) == 0) {
+          if (split) {
+#pragma unroll
+            for (int x = 0; x < 8; ++x)
+              *reinterpret_cast<float4*>(turn + lane * kRowB + (((8 * c + x) ^ (lane & 7)) << 4)) =
+                  make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+          } else {
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
               alignas(16) T y[8];
 #pragma unroll
               for (int e = 0; e < 8; ++e) y[e] = from_f<T>(some ? o[8 * x + e] * il : 0.f);
-              *reinterpret_cast<uint4*>(out + 32 * c + 8 * x) = *reinterpret_cast<const uint4*>(y);
+              *reinterpret_cast<uint4*>(turn + lane * kRowB + (((4 * c + x) ^ (lane & 7)) << 4)) = *reinterpret_cast<const uint4*>(y);
             }
+          }
+          __syncwarp();
+        }
+#pragma unroll 4
+        for (int e = lane; e < 32 * kChunks; e += 32) {
+          const int row = e / kChunks, ch = e % kChunks;
+          const int64_t at = __shfl_sync(0xffffffffu, mine, row);
+          if (!(kept >> row & 1)) continue;
+          const uint4 y = *reinterpret_cast<const uint4*>(turn + row * kRowB + ((ch ^ (row & 7)) << 4));
+          if (split) {
+            *reinterpret_cast<uint4*>(a.part_o + at + p * (kRowB / 4) + ch * 4) = y;
           } else {
+            T* dst = static_cast<T*>(a.out) + at + p * (kRowB / 2) + ch * 8;
+            if (wide) {
+              *reinterpret_cast<uint4*>(dst) = y;
+            } else {
+              alignas(16) T x[8];
+              *reinterpret_cast<uint4*>(x) = y;
 #pragma unroll
-            for (int x = 0; x < 32; ++x) out[32 * c + x] = from_f<T>(some ? o[x] * il : 0.f);
+              for (int k = 0; k < 8; ++k) dst[k] = x[k];
+            }
           }
         }
         __syncwarp();
