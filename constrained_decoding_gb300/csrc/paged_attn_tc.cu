@@ -188,54 +188,67 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
 
   if (warp < 4) {
     regs_down<64>();
-    if (warp == 0 && lane == 0 && nb > 0) {
+    if (warp == 0 && nb > 0) {
       // ------------------------------------------------------------ MMA issuer
+      // The warp stays together and one lane issues, so that descriptors are
+      // computed in uniform registers.
       constexpr uint32_t kIdS = idesc_f16_f32(kTile, kBlock);
       constexpr uint32_t kIdO = idesc_f16_f32(kTile, D) | (1u << 16);  // B (V) is MN-major
       const int nt = two ? 2 : 1;
+      const uint32_t tb = __shfl_sync(0xffffffffu, tbase, 0);
+      const uint64_t dq = sdesc_kmajor_sw128(smem_u32(smem)), dk = sdesc_kmajor_sw128(smem_u32(smem + C::kOffK));
+      const uint64_t dv = sdesc_mnmajor_sw128(smem_u32(smem + C::kOffV), kHalf, 1024);
       auto issue_s = [&](int t, int st) {
         tc_fence_after_sync();
-        const uint32_t qa = smem_u32(smem + t * C::kOp), ka = smem_u32(smem + C::kOffK + st * C::kOp);
+        const uint64_t q = dq + t * (C::kOp >> 4), k0 = dk + st * (C::kOp >> 4);
+        if (elect_one_sync()) {
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t o = (k >> 2) * kHalf + (k & 3) * 32;
-          umma_f16(tbase + t * kBlock, sdesc_kmajor_sw128(qa + o), sdesc_kmajor_sw128(ka + o), kIdS, k > 0 ? 1u : 0u);
+          for (int k = 0; k < D / 16; ++k) {
+            const uint32_t o = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
+            umma_f16(tb + t * kBlock, q + o, k0 + o, kIdS, k > 0 ? 1u : 0u);
+          }
+          umma_commit(&s_full[t]);
+          mbar_arrive(&s_full[t]);  // orders the constants, which the commit alone would not
+          if (t == nt - 1) umma_commit(&k_free[st]);
         }
-        umma_commit(&s_full[t]);
-        mbar_arrive(&s_full[t]);  // orders the constants, which the commit alone would not
-        if (t == nt - 1) umma_commit(&k_free[st]);
+        __syncwarp();
       };
       bool ok = mbar_wait(&k_full[0], 0, kWaitNs);
       for (int t = 0; ok && t < nt; ++t) {
-        ok = mbar_wait(&q_full[t], 0, kWaitNs);
+        ok = __all_sync(0xffffffffu, mbar_wait(&q_full[t], 0, kWaitNs));
         if (ok) issue_s(t, 0);
       }
       for (int i = 0; ok && i < nb; ++i) {
         const int st = i & 1, sn = st ^ 1;
         for (int t = 0; ok && t < nt; ++t) {
           if (t == 0) ok = mbar_wait(&v_full[st], static_cast<uint32_t>((i >> 1) & 1), kWaitNs);
-          ok = ok && mbar_wait(&p_full[t], static_cast<uint32_t>(i & 1), kWaitNs);
+          ok = __all_sync(0xffffffffu, ok && mbar_wait(&p_full[t], static_cast<uint32_t>(i & 1), kWaitNs));
           if (!ok) break;
           tc_fence_after_sync();
-          const uint32_t va = smem_u32(smem + C::kOffV + st * C::kOp);
+          const uint64_t v = dv + st * (C::kOp >> 4);
+          const uint32_t dO = tb + col_o + t * D, dP = tb + t * kBlock, acc = i > 0 ? 1u : 0u;
+          if (elect_one_sync()) {
 #pragma unroll
-          for (int k = 0; k < kBlock / 16; ++k)
-            umma_f16_ts(tbase + col_o + t * D, tbase + t * kBlock + k * 8,
-                        sdesc_mnmajor_sw128(va + k * 16 * 128, kHalf, 1024), kIdO, (i > 0 || k > 0) ? 1u : 0u);
-          umma_commit(&pv_done[t]);
-          if (t == nt - 1) umma_commit(&v_free[st]);
+            for (int k = 0; k < kBlock / 16; ++k)
+              umma_f16_ts(dO, dP + k * 8, v + k * (16 * 128 >> 4), kIdO, k > 0 ? 1u : acc);
+            umma_commit(&pv_done[t]);
+            if (t == nt - 1) umma_commit(&v_free[st]);
+          }
+          __syncwarp();
           if (i + 1 < nb) {
             if (t == 0) ok = mbar_wait(&k_full[sn], static_cast<uint32_t>(((i + 1) >> 1) & 1), kWaitNs);
             // S takes the columns that P V reads its weights from
-            ok = ok && mbar_wait(&pv_done[t], static_cast<uint32_t>(i & 1), kWaitNs);
+            ok = __all_sync(0xffffffffu, ok && mbar_wait(&pv_done[t], static_cast<uint32_t>(i & 1), kWaitNs));
             if (ok) issue_s(t, sn);
           }
         }
-        if (*abort_flag) ok = false;
+        ok = __all_sync(0xffffffffu, ok && !*abort_flag);
       }
-      if (!ok) fail(DEV_WAIT_TIMEOUT_MMA);
-      umma_commit(drain);  // every MMA ends before TMEM is released
-      if (!mbar_wait(drain, 0, kDrainWaitNs)) record_error(a.err, DEV_WAIT_TIMEOUT_DRAIN);
+      if (!ok && lane == 0) fail(DEV_WAIT_TIMEOUT_MMA);
+      if (elect_one_sync()) {
+        umma_commit(drain);  // every MMA ends before TMEM is released
+        if (!mbar_wait(drain, 0, kDrainWaitNs)) record_error(a.err, DEV_WAIT_TIMEOUT_DRAIN);
+      }
     } else if (warp == 1 && nb > 0) {
       // ------------------------------------------------------------ copies of codes, constants of keys
       const int32_t* tab = a.q.table + static_cast<int64_t>(it.seq) * a.q.table_stride;
