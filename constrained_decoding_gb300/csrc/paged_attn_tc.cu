@@ -10,11 +10,10 @@
 //   w = exp2(S sk c + log2 sv - M + 8)   one thread a row
 //   O += w V8                  tcgen05.mma, w (fp16) from TMEM over S's columns
 //   l += w / sv                so out = O / l (see the rows kernel)
-// Each K and V block is converted once for both tiles.  One thread issues all
-// MMAs in the order  P V of a tile, S of its next block, then the other tile:
-// while one tile's rows are in the softmax the tensor cores work for the
-// other.  M moves, and O and l are rescaled, only when a block exceeds it by
-// 2^7.
+// Each K and V block is converted once for both tiles.  The tiles' MMA issuers
+// take turns (P V, then S of the tile's next block): while one tile's rows are
+// in the softmax the tensor cores work for the other.  M moves, and O and l
+// are rescaled, only when a block exceeds it by 2^7.
 //
 // Registers: 512 threads launch with 128 each; the two softmax warpgroups
 // hold a row of 128 scores and take 192, paid for by the other two (64 each):
@@ -117,8 +116,9 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
   uint64_t* q_full = bars + 14;  // [tile] Q rows staged
   uint64_t* raw_full = bars + 16;  // [K, V] codes landed, constants written
   uint64_t* raw_free = bars + 18;  // [K, V] codes converted
-  uint64_t* drain = bars + 20;   // the issuer's MMAs are done
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 21);
+  uint64_t* turn = bars + 20;    // [tile] its issuer's turn
+  uint64_t* drain = bars + 22;   // [tile] its issuer's MMAs are done
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 24);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   float4* sc = reinterpret_cast<float4*>(smem + C::kOffSc);
 
@@ -154,17 +154,18 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
       mbar_init(&k_full[s], 4);
-      mbar_init(&k_free[s], 1);
+      mbar_init(&k_free[s], two ? 2 : 1);
       mbar_init(&v_full[s], 4);
-      mbar_init(&v_free[s], 1);
+      mbar_init(&v_free[s], two ? 2 : 1);
       mbar_init(&s_full[s], 2);
       mbar_init(&p_full[s], 4);
       mbar_init(&pv_done[s], 1);
       mbar_init(&q_full[s], 4);
       mbar_init(&raw_full[s], 1);
+      mbar_init(&turn[s], 1);
+      mbar_init(&drain[s], 1);
       mbar_init(&raw_free[s], 4);
     }
-    mbar_init(drain, 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -188,66 +189,71 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
 
   if (warp < 4) {
     regs_down<64>();
-    if (warp == 0 && nb > 0) {
-      // ------------------------------------------------------------ MMA issuer
-      // The warp stays together and one lane issues, so that descriptors are
-      // computed in uniform registers.
+    if ((warp == 0 || (warp == 2 && two)) && nb > 0) {
+      // ------------------------------------------------------------ MMA issuers, one a tile
+      // They take turns: P V of the tile and S of its next block, then the other
+      // tile, so that one tile's softmax runs under the other's products, and
+      // one's commits under the other's MMAs.  A warp stays together and one lane
+      // issues, so that descriptors are computed in uniform registers.
       constexpr uint32_t kIdS = idesc_f16_f32(kTile, kBlock);
       constexpr uint32_t kIdO = idesc_f16_f32(kTile, D) | (1u << 16);  // B (V) is MN-major
-      const int nt = two ? 2 : 1;
+      const int t = __shfl_sync(0xffffffffu, warp >> 1, 0);
       const uint32_t tb = __shfl_sync(0xffffffffu, tbase, 0);
-      const uint64_t dq = sdesc_kmajor_sw128(smem_u32(smem)), dk = sdesc_kmajor_sw128(smem_u32(smem + C::kOffK));
+      const uint32_t dS = tb + t * kBlock, dO = tb + col_o + t * D;
+      const uint64_t dq = sdesc_kmajor_sw128(smem_u32(smem + t * C::kOp)), dk = sdesc_kmajor_sw128(smem_u32(smem + C::kOffK));
       const uint64_t dv = sdesc_mnmajor_sw128(smem_u32(smem + C::kOffV), kHalf, 1024);
-      auto issue_s = [&](int t, int st) {
+      auto issue_s = [&](int st) {
         tc_fence_after_sync();
-        const uint64_t q = dq + t * (C::kOp >> 4), k0 = dk + st * (C::kOp >> 4);
+        const uint64_t k0 = dk + st * (C::kOp >> 4);
         if (elect_one_sync()) {
 #pragma unroll
           for (int k = 0; k < D / 16; ++k) {
             const uint32_t o = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
-            umma_f16(tb + t * kBlock, q + o, k0 + o, kIdS, k > 0 ? 1u : 0u);
+            umma_f16(dS, dq + o, k0 + o, kIdS, k > 0 ? 1u : 0u);
           }
+          if (two) mbar_arrive(&turn[t ^ 1]);
           umma_commit(&s_full[t]);
           mbar_arrive(&s_full[t]);  // orders the constants, which the commit alone would not
-          if (t == nt - 1) umma_commit(&k_free[st]);
+          umma_commit(&k_free[st]);
         }
         __syncwarp();
       };
-      bool ok = mbar_wait(&k_full[0], 0, kWaitNs);
-      for (int t = 0; ok && t < nt; ++t) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&q_full[t], 0, kWaitNs));
-        if (ok) issue_s(t, 0);
-      }
+      // turn[t] completes once before each of the tile's turns; the first tile's first turn is free
+      bool ok = mbar_wait(&k_full[0], 0, kWaitNs) && mbar_wait(&q_full[t], 0, kWaitNs) &&
+                (t == 0 || mbar_wait(&turn[1], 0, kWaitNs));
+      ok = __all_sync(0xffffffffu, ok);
+      if (ok) issue_s(0);
       for (int i = 0; ok && i < nb; ++i) {
-        const int st = i & 1, sn = st ^ 1;
-        for (int t = 0; ok && t < nt; ++t) {
-          if (t == 0) ok = mbar_wait(&v_full[st], static_cast<uint32_t>((i >> 1) & 1), kWaitNs);
-          ok = __all_sync(0xffffffffu, ok && mbar_wait(&p_full[t], static_cast<uint32_t>(i & 1), kWaitNs));
-          if (!ok) break;
-          tc_fence_after_sync();
-          const uint64_t v = dv + st * (C::kOp >> 4);
-          const uint32_t dO = tb + col_o + t * D, dP = tb + t * kBlock, acc = i > 0 ? 1u : 0u;
-          if (elect_one_sync()) {
+        const int st = i & 1;
+        ok = mbar_wait(&v_full[st], static_cast<uint32_t>((i >> 1) & 1), kWaitNs) &&
+             (!two || mbar_wait(&turn[t], static_cast<uint32_t>((i + t) & 1), kWaitNs)) &&
+             mbar_wait(&p_full[t], static_cast<uint32_t>(i & 1), kWaitNs);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after_sync();
+        const uint64_t v = dv + st * (C::kOp >> 4);
+        const uint32_t acc = i > 0 ? 1u : 0u;
+        if (elect_one_sync()) {
 #pragma unroll
-            for (int k = 0; k < kBlock / 16; ++k)
-              umma_f16_ts(dO, dP + k * 8, v + k * (16 * 128 >> 4), kIdO, k > 0 ? 1u : acc);
-            umma_commit(&pv_done[t]);
-            if (t == nt - 1) umma_commit(&v_free[st]);
-          }
-          __syncwarp();
-          if (i + 1 < nb) {
-            if (t == 0) ok = mbar_wait(&k_full[sn], static_cast<uint32_t>(((i + 1) >> 1) & 1), kWaitNs);
-            // S takes the columns that P V reads its weights from
-            ok = __all_sync(0xffffffffu, ok && mbar_wait(&pv_done[t], static_cast<uint32_t>(i & 1), kWaitNs));
-            if (ok) issue_s(t, sn);
-          }
+          for (int k = 0; k < kBlock / 16; ++k)
+            umma_f16_ts(dO, dS + k * 8, v + k * (16 * 128 >> 4), kIdO, k > 0 ? 1u : acc);
+          umma_commit(&pv_done[t]);
+          umma_commit(&v_free[st]);
+          if (two && i + 1 == nb) mbar_arrive(&turn[t ^ 1]);
         }
-        ok = __all_sync(0xffffffffu, ok && !*abort_flag);
+        __syncwarp();
+        if (i + 1 < nb) {
+          // S takes the columns that P V reads its weights from
+          ok = mbar_wait(&k_full[st ^ 1], static_cast<uint32_t>(((i + 1) >> 1) & 1), kWaitNs) &&
+               mbar_wait(&pv_done[t], static_cast<uint32_t>(i & 1), kWaitNs);
+          ok = __all_sync(0xffffffffu, ok && !*abort_flag);
+          if (ok) issue_s(st ^ 1);
+        }
       }
       if (!ok && lane == 0) fail(DEV_WAIT_TIMEOUT_MMA);
       if (elect_one_sync()) {
-        umma_commit(drain);  // every MMA ends before TMEM is released
-        if (!mbar_wait(drain, 0, kDrainWaitNs)) record_error(a.err, DEV_WAIT_TIMEOUT_DRAIN);
+        umma_commit(&drain[t]);  // every MMA ends before TMEM is released
+        if (!mbar_wait(&drain[t], 0, kDrainWaitNs)) record_error(a.err, DEV_WAIT_TIMEOUT_DRAIN);
       }
     } else if (warp == 1 && nb > 0) {
       // ------------------------------------------------------------ copies of codes, constants of keys
