@@ -47,7 +47,8 @@ struct TileCfg {
   static constexpr int kRaw = kBlock * D;               // a block's K or V codes
   static constexpr int kOffRaw = kOffV + 2 * kOp;       // K's, then V's
   static constexpr int kOffSc = kOffRaw + 2 * kRaw;     // [4][8] float4: constants of 16 keys
-  static constexpr int kOffBar = kOffSc + 4 * 8 * 16;
+  static constexpr int kOffWhole = kOffSc + 4 * 8 * 16;  // [4]: is every key of the block there?
+  static constexpr int kOffBar = kOffWhole + 16;
   static constexpr int kSmem = kOffBar + 256 + 1024;    // + alignment slack
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
 };
@@ -121,6 +122,7 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 24);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   float4* sc = reinterpret_cast<float4*>(smem + C::kOffSc);
+  volatile int* whole_block = reinterpret_cast<volatile int*>(smem + C::kOffWhole);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int hk = blockIdx.y, z = blockIdx.z;
@@ -285,14 +287,19 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
             // 16 keys to a lane: K scale, log2 and reciprocal of the V scale, seen or not
             const int pl = lane * 16 >> a.c.page_log2;
             const int cid = __shfl_sync(0xffffffffu, good ? id : -1, pl & 31);
+            const bool there = cid >= 0 && j0 + lane * 16 < len;
+            const uint32_t all = __ballot_sync(0xffffffffu, there) & 0xffu;
+            // block i - 4 has left the softmax: K of block i - 1 was converted, for which every S of block i - 3
+            // was done, each of which came after the P V of block i - 4
             if (lane < kBlock / 16) {
               float4 c = make_float4(0.f, 0.f, 0.f, 0.f);
-              if (cid >= 0 && j0 + lane * 16 < len) {
+              if (there) {
                 float v = a.c.vs[static_cast<int64_t>(cid) * a.c.Hkv + hk];
                 if (v < kScaleFloor) v = kScaleFloor;  // a NaN stays
                 c = make_float4(a.c.ks[static_cast<int64_t>(cid) * a.c.Hkv + hk], lg2(v), 1.f / v, 1.f);
               }
-              sc[(i & 3) * 8 + lane] = c;  // block i - 4 left the softmax before V of block i - 2 was converted
+              sc[(i & 3) * 8 + lane] = c;
+              if (lane == 0) whole_block[i & 3] = all == 0xffu && len - j0 >= kBlock;
             }
             __syncwarp();
           }
@@ -337,9 +344,7 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
         if (ok && i >= 2) ok = mbar_wait(kv ? &v_free[st] : &k_free[st], static_cast<uint32_t>(((i - 2) >> 1) & 1), kWaitNs);
         ok = __all_sync(0xffffffffu, ok && !*abort_flag);
         if (!ok) break;
-        bool whole = live == kBlock;
-#pragma unroll
-        for (int g = 0; g < 8; ++g) whole = whole && sc[(i & 3) * 8 + g].w != 0.f;
+        const bool whole = whole_block[i & 3] != 0;
         const uint8_t* src = raw0 + kv * C::kRaw;
         uint8_t* dst = smem + (kv ? C::kOffV : C::kOffK) + st * C::kOp;
 #pragma unroll
@@ -444,12 +449,11 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
         const float4* cs = sc + (i & 3) * 8;
         tmem_ld_wait();
         const int j0 = (b0 + i) * kBlock;
-        bool plain = j0 + kBlock <= wmin;
+        const bool plain = whole_block[i & 3] != 0 && j0 + kBlock <= wmin;
         float mx = -INFINITY;
 #pragma unroll
         for (int g = 0; g < 8; ++g) {
           const float4 k = cs[g];
-          plain = plain && k.w != 0.f;
           float m = max3(s[16 * g], s[16 * g + 1], s[16 * g + 2]), m1 = max3(s[16 * g + 3], s[16 * g + 4], s[16 * g + 5]);
 #pragma unroll
           for (int e = 6; e < 14; e += 4) {
