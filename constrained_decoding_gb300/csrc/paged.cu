@@ -21,7 +21,8 @@ namespace {
 // as exact at position 2^31 as at 1.  Bound by the bytes of x and y: a thread
 // owns the same VEC channels (and their partners, rot / 2 further, in the half
 // layout) of every hgs-th head of one token, so an angle's sine and cosine are
-// computed once for all of them, and takes four heads' loads at a time.
+// computed once for all of them, and takes two heads' loads at a time (four cost
+// registers and 4 us of 25 at 8192 tokens x 32 heads).
 // VEC: the widest access that pointers, strides and the pair layout allow.
 template <class T, int N>
 struct alignas(sizeof(T) * N) Chunk {
@@ -33,7 +34,7 @@ __global__ void __launch_bounds__(256) rope_kernel(RopeKArgs a, unsigned units, 
   constexpr int kN = INTER && VEC == 1 ? 2 : VEC;   // channels of a chunk of the rotated part
   constexpr int kL = INTER && VEC == 1 ? 1 : VEC;   // channels of one access
   constexpr int kPairs = INTER ? kN / 2 : kN;
-  constexpr int kHeads = 4;
+  constexpr int kHeads = 2;
   griddep_launch_dependents();
   griddep_wait();
   const unsigned idx = blockIdx.x * 256u + threadIdx.x;
@@ -172,9 +173,8 @@ struct AppendBlock {
   uint8_t* dst;
   float* scale;
 };
-__device__ __forceinline__ bool append_block(const AppendArgs& a, bool is_v, AppendBlock* b) {
+__device__ __forceinline__ bool append_block(const AppendArgs& a, bool is_v, int h, AppendBlock* b) {
   const int page = 1 << a.c.page_log2;
-  const int h = blockIdx.y;
   // item -> (sequence, page of its new range)
   const SeqItem it = find_item(a.q, static_cast<int>(blockIdx.x), 1, a.c.page_log2, 2);
   if (it.seq < 0) return false;
@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_any_kernel(AppendArg
   griddep_wait();
   const bool is_v = blockIdx.z != 0;
   AppendBlock b;
-  if (!append_block(a, is_v, &b)) return;
+  if (!append_block(a, is_v, static_cast<int>(blockIdx.y), &b)) return;
   const int D = a.c.dim, total = b.rows * D;
   const T* src = static_cast<const T*>(is_v ? a.v : a.k) + (is_v ? a.v_head : a.k_head) * blockIdx.y;
   const int64_t ts = is_v ? a.v_tok : a.k_tok;
@@ -256,98 +256,143 @@ __global__ void __launch_bounds__(kAppendThreads) kv_append_any_kernel(AppendArg
     b.dst[(b.held + e / D) * a.c.tok_stride + e % D] = encode(value(e / D, e % D) * inv, a.c.format);
 }
 
-__device__ __forceinline__ void append_turn(const RopeSpec& rope, int p, int pair, float& x, float& y) {
-  float c, s;
-  turn(p, rope.freqs[pair], &c, &s);
-  c *= rope.amp;
-  s *= rope.amp;
-  const float x0 = x, y0 = y;
-  x = x0 * c - y0 * s;
-  y = y0 * c + x0 * s;
-}
-
 // Rows of whole 16-byte chunks: a thread holds NU units of a row's 16 channels
 // (two 8-channel chunks, the partners of the half layout's pairs) in registers
-// between the maximum and the codes, so each row is read once.
-template <class T, int NU>
+// between the maximum and the codes, so each row is read once.  A CTA takes HB
+// heads of a page, with the same sines and cosines, and loads the next head's
+// rows before it works on the present one's: what bounds a block by itself is
+// the chain of loads that finds it.
+template <class T, int NU, int HB>
 __global__ void __launch_bounds__(256) kv_append_kernel(AppendArgs a) {
   griddep_launch_dependents();
   griddep_wait();
   const bool is_v = blockIdx.z != 0;
+  const int h0 = static_cast<int>(blockIdx.y) * HB;
   AppendBlock b;
-  if (!append_block(a, is_v, &b)) return;
+  if (!append_block(a, is_v, h0, &b)) return;
   const int ulog = a.c.dim == 128 ? 3 : 2;  // units of a row: dim / 16
   const int nr = is_v ? 0 : a.rope.rot / 8;  // rotated chunks
   const bool inter = a.rope.interleaved != 0;
-  const T* src = static_cast<const T*>(is_v ? a.v : a.k) + (is_v ? a.v_head : a.k_head) * blockIdx.y;
-  const int64_t ts = is_v ? a.v_tok : a.k_tok;
-  float v[NU][16];
-  uint32_t am = 0;
+  const int64_t ts = is_v ? a.v_tok : a.k_tok, hs = is_v ? a.v_head : a.k_head;
+  const int u = threadIdx.x & ((1 << ulog) - 1);  // blockDim.x is a multiple of a row's units
+  const bool pairs = !inter && u < nr / 2;        // chunks whose channels turn with one another's
+  const bool near1 = inter && 2 * u < nr, near2 = inter && 2 * u + 1 < nr;  // ... neighbours in the first, in both
+  const int ca = pairs ? u : 2 * u, cb = pairs ? u + nr / 2 : ca + 1;
+  const T* src = static_cast<const T*>(is_v ? a.v : a.k) + hs * h0 + static_cast<int64_t>(b.row0) * ts;
+  Eight<T> x[NU][2];
+  auto fetch = [&](const T* p) {
 #pragma unroll
-  for (int k = 0; k < NU; ++k) {
-    const int e = threadIdx.x + k * blockDim.x, r = e >> ulog, u = e & ((1 << ulog) - 1);
-    const bool here = r < b.rows;
-    const bool pairs = !inter && u < nr / 2;  // chunks whose channels turn with one another's
-    const int ca = pairs ? u : 2 * u, cb = pairs ? u + nr / 2 : ca + 1;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) v[k][i] = 0.f;
-    if (here) {
-      const T* row = src + (b.row0 + r) * ts;
-      load8(row + ca * 8, v[k]);
-      load8(row + cb * 8, v[k] + 8);
-    }
-    const int p = !here ? 0 : a.pos ? a.pos[b.row0 + r] : b.pos0 + r;
-    if (here && pairs) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) append_turn(a.rope, p, ca * 8 + i, v[k][i], v[k][8 + i]);
-    } else if (here && inter && ca < nr) {  // neighbours; the second chunk's only if it turns too
-#pragma unroll
-      for (int i = 0; i < 4; ++i) append_turn(a.rope, p, ca * 4 + i, v[k][2 * i], v[k][2 * i + 1]);
-      if (cb < nr) {
-#pragma unroll
-        for (int i = 4; i < 8; ++i) append_turn(a.rope, p, ca * 4 + i, v[k][2 * i], v[k][2 * i + 1]);
+    for (int k = 0; k < NU; ++k) {
+      const int r = (threadIdx.x + k * blockDim.x) >> ulog;
+      if (r < b.rows) {
+        load8(p + r * ts + ca * 8, &x[k][0]);
+        load8(p + r * ts + cb * 8, &x[k][1]);
       }
     }
+  };
+  fetch(src);
+  float cs[NU][8], sn[NU][8];
+  if (pairs || near1) {
 #pragma unroll
-    for (int i = 0; i < 16; ++i) am = max(am, __float_as_uint(v[k][i]) & 0x7fffffffu);
-  }
-  const float inv = 1.f / append_scale(a, b, am);
+    for (int k = 0; k < NU; ++k) {
+      const int r = (threadIdx.x + k * blockDim.x) >> ulog;
+      if (r < b.rows) {
+        const int p = a.pos ? a.pos[b.row0 + r] : b.pos0 + r;
 #pragma unroll
-  for (int k = 0; k < NU; ++k) {
-    const int e = threadIdx.x + k * blockDim.x, r = e >> ulog, u = e & ((1 << ulog) - 1);
-    const bool pairs = !inter && u < nr / 2;
-    const int ca = pairs ? u : 2 * u, cb = pairs ? u + nr / 2 : ca + 1;
-    if (r < b.rows) {
-      uint8_t* row = b.dst + (b.held + r) * a.c.tok_stride;
-      *reinterpret_cast<uint2*>(row + ca * 8) = encode8(v[k], inv, a.c.format);
-      *reinterpret_cast<uint2*>(row + cb * 8) = encode8(v[k] + 8, inv, a.c.format);
+        for (int i = 0; i < 8; ++i) {
+          const int pair = pairs ? ca * 8 + i : min(ca * 4 + i, a.rope.rot / 2 - 1);
+          turn(p, a.rope.freqs[pair], &cs[k][i], &sn[k][i]);
+          cs[k][i] *= a.rope.amp;
+          sn[k][i] *= a.rope.amp;
+        }
+      }
     }
+  }
+#pragma unroll 1
+  for (int h = h0;; ++h) {
+    float v[NU][16];
+    float am = 0.f;
+#pragma unroll
+    for (int k = 0; k < NU; ++k) {
+      const int r = (threadIdx.x + k * blockDim.x) >> ulog;
+      if (r < b.rows) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) v[k][i] = to_f(x[k][i >> 3].v[i & 7]);
+        if (pairs) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float p = v[k][i], q = v[k][8 + i];
+            v[k][i] = p * cs[k][i] - q * sn[k][i];
+            v[k][8 + i] = q * cs[k][i] + p * sn[k][i];
+          }
+        } else if (near1) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            if (i >= 4 && !near2) break;
+            const float p = v[k][2 * i], q = v[k][2 * i + 1];
+            v[k][2 * i] = p * cs[k][i] - q * sn[k][i];
+            v[k][2 * i + 1] = q * cs[k][i] + p * sn[k][i];
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < 16; i += 2) am = max_abs(am, v[k][i], v[k][i + 1]);
+      }
+    }
+    const bool more = h + 1 < min(h0 + HB, a.c.Hkv);
+    if (HB > 1 && more) {
+      src += hs;
+      fetch(src);
+    }
+    const float scale = append_scale(a, b, __float_as_uint(am) & 0x7fffffffu);
+    const bool finite = fabsf(scale) < INFINITY;
+    const float inv = 1.f / scale;
+#pragma unroll
+    for (int k = 0; k < NU; ++k) {
+      const int r = (threadIdx.x + k * blockDim.x) >> ulog;
+      if (r < b.rows) {
+        uint8_t* row = b.dst + (b.held + r) * a.c.tok_stride;
+        *reinterpret_cast<uint2*>(row + ca * 8) = finite ? encode8(v[k], inv, a.c.format) : make_uint2(0u, 0u);
+        *reinterpret_cast<uint2*>(row + cb * 8) = finite ? encode8(v[k] + 8, inv, a.c.format) : make_uint2(0u, 0u);
+      }
+    }
+    if (HB == 1 || !more) return;
+    b.dst += a.c.head_stride;
+    b.scale += 1;
+    __syncthreads();  // the blocks' maxima are exchanged in one place
   }
 }
 
+template <class T, int HB>
+int launch_append_h(const AppendArgs& a, unsigned items, cudaStream_t s) {
+  const int units = (a.c.dim / 16) << a.c.page_log2;  // of a full block: 64 .. 1024
+  const dim3 grid(items, static_cast<unsigned>((a.c.Hkv + HB - 1) / HB), 2);
+  if (units <= 256) return launch_k(kv_append_kernel<T, 1, HB>, grid, dim3(static_cast<unsigned>(units)), 0, s, a);
+  if (units == 512) return launch_k(kv_append_kernel<T, 2, HB>, grid, dim3(256), 0, s, a);
+  return launch_k(kv_append_kernel<T, 4, HB>, grid, dim3(256), 0, s, a);
+}
+
 template <class T>
-int launch_append_t(const AppendArgs& a, cudaStream_t s) {
-  const dim3 grid(static_cast<unsigned>((static_cast<int64_t>(a.q.n_tok) >> a.c.page_log2) + 2ll * a.q.n_seq),
-                  static_cast<unsigned>(a.c.Hkv), 2);
+int launch_append_t(const AppendArgs& a, int sms, cudaStream_t s) {
+  const unsigned items = static_cast<unsigned>((static_cast<int64_t>(a.q.n_tok) >> a.c.page_log2) + 2ll * a.q.n_seq);
   // 16-byte chunks: 8 channels (4 of fp32, loaded in twos)
   uint64_t m = reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v);
   m |= static_cast<uint64_t>(a.k_tok | a.k_head | a.v_tok | a.v_head) * sizeof(T);
   const bool chunks = m % 16 == 0 && a.rope.rot % (a.rope.interleaved ? 8 : 16) == 0;
-  if (!chunks) return launch_k(kv_append_any_kernel<T>, grid, dim3(kAppendThreads), 0, s, a);
-  const int units = (a.c.dim / 16) << a.c.page_log2;  // of a full block: 64 .. 1024
-  if (units <= 256) return launch_k(kv_append_kernel<T, 1>, grid, dim3(static_cast<unsigned>(units)), 0, s, a);
-  if (units == 512) return launch_k(kv_append_kernel<T, 2>, grid, dim3(256), 0, s, a);
-  return launch_k(kv_append_kernel<T, 4>, grid, dim3(256), 0, s, a);
+  if (!chunks)
+    return launch_k(kv_append_any_kernel<T>, dim3(items, static_cast<unsigned>(a.c.Hkv), 2), dim3(kAppendThreads), 0, s, a);
+  // several heads a CTA where the pages alone fill the GPU
+  const int64_t pages = static_cast<int64_t>(a.q.n_tok) >> a.c.page_log2;
+  return 2 * pages >= 2ll * sms ? launch_append_h<T, 4>(a, items, s) : launch_append_h<T, 1>(a, items, s);
 }
 
 }  // namespace
 
-int launch_kv_append(const AppendArgs& a, cudaStream_t s) {
+int launch_kv_append(const AppendArgs& a, int sms, cudaStream_t s) {
   if (a.q.n_tok == 0 || a.q.n_seq == 0) return 0;
   switch (a.dtype) {
-    case PCD_DTYPE_F32: return launch_append_t<float>(a, s);
-    case PCD_DTYPE_BF16: return launch_append_t<__nv_bfloat16>(a, s);
-    default: return launch_append_t<__half>(a, s);
+    case PCD_DTYPE_F32: return launch_append_t<float>(a, sms, s);
+    case PCD_DTYPE_BF16: return launch_append_t<__nv_bfloat16>(a, sms, s);
+    default: return launch_append_t<__half>(a, sms, s);
   }
 }
 

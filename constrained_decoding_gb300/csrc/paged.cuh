@@ -128,38 +128,44 @@ __device__ __forceinline__ float decode(uint8_t q, int format) {
   return __half2float(__half(__nv_cvt_fp8_to_halfraw(q, __NV_E4M3)));
 }
 
-// Eight values and their codes.
+// Eight values as they are stored, and in fp32.
 template <class T>
-__device__ __forceinline__ void load8(const T* p, float* v) {
-  if constexpr (sizeof(T) == 4) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
-  } else {
-    alignas(16) T x[8];
-    *reinterpret_cast<uint4*>(x) = *reinterpret_cast<const uint4*>(p);
+struct alignas(16) Eight {
+  T v[8];
+};
+template <class T>
+__device__ __forceinline__ void load8(const T* p, Eight<T>* e) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = to_f(x[i]);
-  }
+  for (int i = 0; i < static_cast<int>(sizeof(T)) / 2; ++i)
+    reinterpret_cast<uint4*>(e)[i] = reinterpret_cast<const uint4*>(p)[i];
 }
+// Their codes at a finite scale (so no value is a NaN or beyond the largest
+// code).  int8: the product rounded to an integer by adding 1.5 2^23, whose low
+// byte then is the code.
 __device__ __forceinline__ uint2 encode8(const float* v, float inv, int format) {
   uint32_t w[2];
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
-    w[j] = 0;
+    float x[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] = v[4 * j + i] * inv;
     if (format == PCD_KV_INT8) {
+      uint32_t n[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) w[j] |= static_cast<uint32_t>(encode(v[4 * j + i] * inv, PCD_KV_INT8)) << (8 * i);
+      for (int i = 0; i < 4; ++i) n[i] = __float_as_uint(__fadd_rn(x[i], 12582912.f));
+      w[j] = __byte_perm(__byte_perm(n[0], n[1], 0x0040), __byte_perm(n[2], n[3], 0x0040), 0x5410);
     } else {
-#pragma unroll
-      for (int i = 0; i < 4; i += 2) {
-        float x = v[4 * j + i] * inv, y = v[4 * j + i + 1] * inv;
-        if (x != x) x = 0.f;  // as encode()
-        if (y != y) y = 0.f;
-        w[j] |= static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3)) << (8 * i);
-      }
+      w[j] = static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(x[0], x[1]), __NV_SATFINITE, __NV_E4M3)) |
+             static_cast<uint32_t>(__nv_cvt_float2_to_fp8x2(make_float2(x[2], x[3]), __NV_SATFINITE, __NV_E4M3)) << 16;
     }
   }
   return make_uint2(w[0], w[1]);
+}
+// The larger magnitude; a NaN wins.
+__device__ __forceinline__ float max_abs(float m, float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(fabsf(a)), "f"(fabsf(b)));
+  return r;
 }
 
 // Codes as fp16, exactly.  e4m3 by the conversion instruction (64 lanes a

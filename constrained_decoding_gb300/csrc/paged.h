@@ -56,7 +56,7 @@ struct AppendArgs {
   const int32_t* pos;  // per new token, or nullptr: its place in the cache
   int* err;
 };
-int launch_kv_append(const AppendArgs& a, cudaStream_t s);
+int launch_kv_append(const AppendArgs& a, int sms, cudaStream_t s);
 
 // How a call is cut up.  rows: query rows of a work item (16: warp MMA, 256:
 // tcgen05).  n_splits: ranges that every item's keys are divided into, walked

@@ -196,7 +196,7 @@ extern "C" int pcd_k_kv_append(const pcd_kv_pages* cache, const void* k, const v
   a.k_tok = k_tok, a.k_head = k_head, a.v_tok = v_tok, a.v_head = v_head;
   a.pos = pos;
   a.err = dev_err;
-  return launched(pcd::launch_kv_append(a, static_cast<cudaStream_t>(stream)));
+  return launched(pcd::launch_kv_append(a, device_sms(), static_cast<cudaStream_t>(stream)));
 }
 
 namespace {
