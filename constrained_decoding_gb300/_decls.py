@@ -84,11 +84,11 @@ SIGNATURES = [
     ("pcd_rope_freqs", c_int, [c_int, c_double, c_int, c_double, c_double, c_double, c_double, c_void_p, P(c_float)]),
     ("pcd_k_rope", c_int, [c_void_p, c_void_p, c_int, c_int, c_int, c_int, c_int64, c_int64, c_int64, c_int64, c_void_p,
                            c_int, c_int, c_float, c_void_p, c_int, c_int, c_void_p]),
-    ("pcd_k_kv_append", c_int, [P(pcd_kv_pages), c_void_p, c_void_p, c_int, c_int64, c_int64, c_int64, c_int64,
+    ("pcd_k_kv_append", c_int, [c_void_p, c_void_p, c_void_p, c_int, c_int64, c_int64, c_int64, c_int64,
                                 c_void_p, c_void_p, c_void_p, c_int, c_int, c_int, c_void_p, c_int, c_int, c_float,
                                 c_void_p, c_void_p, c_void_p]),
     ("pcd_k_paged_attention_scratch_bytes", c_int64, [c_int, c_int, c_int, c_int, c_int, c_int64]),
-    ("pcd_k_paged_attention", c_int, [P(pcd_kv_pages), c_void_p, c_void_p, c_void_p, c_int, c_int, c_int64, c_int64,
+    ("pcd_k_paged_attention", c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_int, c_int64, c_int64,
                                       c_int64, c_int64, c_void_p, c_void_p, c_void_p, c_int, c_int, c_int, c_int64,
                                       c_int, c_float, c_void_p, c_int64, c_void_p, c_void_p]),
 ]

@@ -20,11 +20,12 @@ that keep channels contiguous, the same for both) and two float32 scales
 from __future__ import annotations
 
 import ctypes
+import functools
+import struct
 from typing import Optional
 
 import torch
 
-from . import _decls as D
 from ._lib import load
 from .pcd import PCDError, _check
 
@@ -123,8 +124,11 @@ def pcd_k_rope(x, freqs, pos=None, *, base: int = 0, interleaved: bool = False, 
     return out
 
 
+_PAGES = struct.Struct("@4P3q5i4x")  # pcd_kv_pages
+
+
 def _pages(k_cache, v_cache, k_scale, v_scale):
-    """(struct, device, type) of a cache."""
+    """(pcd_kv_pages as bytes, device, page size, KV heads, head dim) of a cache."""
     shape, dtype, dev, st = k_cache.shape, k_cache.dtype, k_cache.get_device(), k_cache.stride()
     fmt = _FORMAT.get(dtype)
     if fmt is None or dev < 0 or len(shape) != 4:
@@ -135,8 +139,9 @@ def _pages(k_cache, v_cache, k_scale, v_scale):
     for t in (k_scale, v_scale):
         if t.dtype is not _float32 or t.get_device() != dev or t.shape != two or not t.is_contiguous():
             raise ValueError("scales: contiguous float32 [pages, KV heads] on the cache's device")
-    return D.pcd_kv_pages(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), st[0], st[1],
-                          st[2], shape[0], shape[2], shape[1], shape[3], fmt), dev
+    pages, heads, size, dim = shape
+    return _PAGES.pack(k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), st[0], st[1], st[2],
+                       pages, size, heads, dim, fmt), dev, size, heads, dim
 
 
 def _table(table, n_seq: int, dev: int):
@@ -156,16 +161,16 @@ def pcd_k_kv_append(k, v, k_cache, v_cache, k_scale, v_scale, q_off, kv_len, tab
     kv_len[s] with them; token j of it lies in page table[s, j // page size].
     `err` (int32, one element) is set nonzero when offsets, lengths or pages
     were out of range."""
-    c, dev = _pages(k_cache, v_cache, k_scale, v_scale)
+    c, dev, _, kv_heads, dim = _pages(k_cache, v_cache, k_scale, v_scale)
     dtype, shape, n_seq = k.dtype, k.shape, kv_len.numel()
     code = _DTYPE.get(dtype)
-    if code is None or len(shape) != 3 or shape[1] != c.n_kv_heads or shape[2] != c.head_dim:
+    if code is None or len(shape) != 3 or shape[1] != kv_heads or shape[2] != dim:
         raise ValueError("k: float32, float16 or bfloat16 [tokens, KV heads, head dim]")
     n = shape[0]
     ks, vs = _rows(k, dev, shape, dtype, "k"), _rows(v, dev, shape, dtype, "v")
     t, t_stride, _ = _table(table, n_seq, dev)
-    f, rot = _rope(freqs, dev, shape[2])
-    _launch(dev, "pcd_k_kv_append", _lib.pcd_k_kv_append, ctypes.byref(c), k.data_ptr(), v.data_ptr(), code, ks[0], ks[1],
+    f, rot = _rope(freqs, dev, dim)
+    _launch(dev, "pcd_k_kv_append", _lib.pcd_k_kv_append, c, k.data_ptr(), v.data_ptr(), code, ks[0], ks[1],
             vs[0], vs[1], _ints(q_off, dev, n_seq + 1, "q_off"), _ints(kv_len, dev, n_seq, "kv_len"), t, n_seq, n, t_stride,
             f, rot, interleaved, amp, _ints(pos, dev, n, "pos"), _ints(err, dev, 1, "err"))
 
@@ -175,7 +180,9 @@ def pcd_k_paged_attention_scratch_bytes(n_tok: int, n_seq: int, n_q_heads: int, 
     return int(_lib.pcd_k_paged_attention_scratch_bytes(n_tok, n_seq, n_q_heads, n_kv_heads, head_dim, max_kv))
 
 
+@functools.lru_cache(maxsize=1024)
 def _scratch_bytes(dev: int, *sizes) -> int:
+    """What a call of these sizes needs on this device: a function of them alone."""
     if _current_device() == dev:
         return _lib.pcd_k_paged_attention_scratch_bytes(*sizes)
     with torch.cuda.device(dev):
@@ -193,9 +200,8 @@ def pcd_k_paged_attention(q, k_cache, v_cache, k_scale, v_scale, q_off, kv_len, 
     defaults to head_dim ** -0.5.  Returns the output, and with return_lse the
     log-sum-exp [tokens, query heads] too.  `scratch` (uint8) replaces the
     workspace that is otherwise taken from torch's allocator."""
-    c, dev = _pages(k_cache, v_cache, k_scale, v_scale)
+    c, dev, page, kv_heads, dim = _pages(k_cache, v_cache, k_scale, v_scale)
     dtype, shape, n_seq = q.dtype, q.shape, kv_len.numel()
-    dim = c.head_dim
     if (dtype is not torch.float16 and dtype is not torch.bfloat16) or len(shape) != 3 or shape[2] != dim:
         raise ValueError("q: float16 or bfloat16 [tokens, heads, head dim]")
     n, heads, _ = shape
@@ -208,16 +214,16 @@ def pcd_k_paged_attention(q, k_cache, v_cache, k_scale, v_scale, q_off, kv_len, 
         os = _rows(out, dev, shape, dtype, "out")
     lse = torch.empty((n, heads), dtype=_float32, device=q.device) if return_lse else None
     if max_kv is None:
-        max_kv = width * c.page_size
+        max_kv = width * page
     if scratch is None:
-        need = _scratch_bytes(dev, n, n_seq, heads, c.n_kv_heads, dim, max_kv)
+        need = _scratch_bytes(dev, n, n_seq, heads, kv_heads, dim, max_kv)
         if need > 0:
             scratch = torch.empty(need, dtype=torch.uint8, device=q.device)
     elif scratch.get_device() != dev or not scratch.is_contiguous():
         raise ValueError(f"scratch: contiguous bytes on cuda:{dev}")
     else:
         need = scratch.numel() * scratch.element_size()
-    _launch(dev, "pcd_k_paged_attention", _lib.pcd_k_paged_attention, ctypes.byref(c), q.data_ptr(), out.data_ptr(),
+    _launch(dev, "pcd_k_paged_attention", _lib.pcd_k_paged_attention, c, q.data_ptr(), out.data_ptr(),
             lse.data_ptr() if return_lse else 0, _DTYPE[dtype], heads, qs[0], qs[1], os[0], os[1],
             _ints(q_off, dev, n_seq + 1, "q_off"), _ints(kv_len, dev, n_seq, "kv_len"), t, n_seq, n, t_stride, max_kv, causal,
             dim ** -0.5 if scale is None else scale, 0 if scratch is None else scratch.data_ptr(), need,

@@ -135,6 +135,17 @@ def test_attention_refuses(lib, kw):
     assert lib.pcd_last_error()
 
 
+def test_binding_packs_the_struct_of_the_header(lib):
+    """The binding's packed pcd_kv_pages has the layout of its declaration."""
+    from constrained_decoding_gb300 import _decls as D
+    from constrained_decoding_gb300 import paged
+    vals = (11, 12, 13, 14, 21, 22, 23, 31, 32, 33, 34, 35)
+    raw = paged._PAGES.pack(*vals)
+    assert len(raw) == ctypes.sizeof(D.pcd_kv_pages)
+    c = D.pcd_kv_pages.from_buffer_copy(raw)
+    assert tuple(getattr(c, n) for n, _ in D.pcd_kv_pages._fields_) == vals
+
+
 def test_empty_calls(lib):
     assert append(lib, n=0, k=None, v=None) == 0 and append(lib, n_seq=0, n=3) == 0
     assert attend(lib, n=0, q=None, out=None) == 0 and attend(lib, n_seq=0) == 0
