@@ -424,7 +424,7 @@ namespace {
 // ragged lengths leave nobody idle; states of items that a stretch's end cuts go
 // to scratch, and a second kernel joins them.
 constexpr float kSlack = 7.f;
-constexpr int kWarps = 4, kStagesR = 4;
+constexpr int kWarps = 4, kStagesR = 3;
 
 template <int D>
 struct RowsCfg {
@@ -466,7 +466,7 @@ __device__ __forceinline__ int64_t rows_units(const PagedAttnArgs& a, const Rows
 template <int D, int FMT, class T>
 __global__ void __launch_bounds__(kWarps * 32, 3) paged_attn_rows_kernel(PagedAttnArgs a) {
   using C = RowsCfg<D>;
-  extern __shared__ __align__(16) uint8_t smem[];
+  extern __shared__ __align__(128) uint8_t smem[];
   griddep_launch_dependents();
   griddep_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -586,8 +586,12 @@ __global__ void __launch_bounds__(kWarps * 32, 3) paged_attn_rows_kernel(PagedAt
   const int step = static_cast<int>(a.c.tok_stride) * (32 / kCh);
   const uint8_t* ksrc = a.c.k + hk * a.c.head_stride + key0 * a.c.tok_stride + ch * 16;
   const int64_t vdelta = a.c.v - a.c.k;
-  uint32_t kdst = smem_u32(ring) + key0 * D + ((ch ^ ((key0 & 1) << 2)) & (kCh - 1)) * 16;
+  // shared places of key0's chunks; later keys keep K's swizzle, and V's but for its upper bit
+  const uint32_t kdst = smem_u32(ring) + key0 * D + ((ch ^ ((key0 & 1) << 2)) & (kCh - 1)) * 16;
+  const uint32_t vdst = smem_u32(ring) + 16 * D + key0 * D + ((ch ^ (((key0 >> 1) & 3) << 1)) & (kCh - 1)) * 16;
+  auto v_place = [](uint32_t p, int e) { return D == 128 && (e & 1) ? p ^ 64u : p; };
   int ids_at = 0;  // `ids` holds blocks ids_at ..
+  uint32_t fill = 0;
   auto issue = [&](int i) {
     if (i < nb) {
       if (i - ids_at >= 32) {
@@ -599,23 +603,28 @@ __global__ void __launch_bounds__(kWarps * 32, 3) paged_attn_rows_kernel(PagedAt
       const int j0 = block_at(i) << 4;
       const int slot = j0 & ((1 << a.c.page_log2) - 1);
       const uint8_t* src = ksrc + max(id, 0) * a.c.page_stride + slot * a.c.tok_stride;
-      const uint32_t st = (i % kStagesR) * C::kStage;
+      if (id >= 0 && j0 + 16 <= len) {
 #pragma unroll
-      for (int e = 0; e < kCh / 2; ++e) {
-        const int key = key0 + e * (32 / kCh);
-        // slots behind the last token read as zeros, whatever they hold
-        const int bytes = id >= 0 && j0 + key < len ? 16 : 0;
-        cp_async16_to(kdst + st + e * (32 / kCh) * D, src + e * step, bytes);
-        cp_async16_to(smem_u32(ring) + st + 16 * D + key * D + ((ch ^ (((key >> 1) & 3) << 1)) & (kCh - 1)) * 16,
-                      src + vdelta + e * step, bytes);
+        for (int e = 0; e < kCh / 2; ++e) {
+          cp_async16_to(kdst + fill + e * (32 / kCh) * D, src + e * step, 16);
+          cp_async16_to(v_place(vdst, e) + fill + e * (32 / kCh) * D, src + vdelta + e * step, 16);
+        }
+      } else {  // slots behind the last token, and pages the table has wrong, read as zeros
+#pragma unroll
+        for (int e = 0; e < kCh / 2; ++e) {
+          const int bytes = id >= 0 && j0 + key0 + e * (32 / kCh) < len ? 16 : 0;
+          cp_async16_to(kdst + fill + e * (32 / kCh) * D, src + e * step, bytes);
+          cp_async16_to(v_place(vdst, e) + fill + e * (32 / kCh) * D, src + vdelta + e * step, bytes);
+        }
       }
     }
     cp_async_commit();
+    fill = fill + C::kStage == kStagesR * C::kStage ? 0u : fill + C::kStage;
   };
 #pragma unroll 1
   for (int i = 0; i < kStagesR - 1; ++i) issue(i);
   scales(ids);
-  int sc_at = 0;
+  int sc_at = 0, drain = 0;
 
   // ---- Q fragments: k-step t takes channels (64 * (t / 4) + 16 c + 4 (t % 4)) + {0, 1 | 2, 3}
   uint32_t qf[D / 16][4];
@@ -685,7 +694,8 @@ __global__ void __launch_bounds__(kWarps * 32, 3) paged_attn_rows_kernel(PagedAt
     const float bsk = __shfl_sync(0xffffffffu, sk, i - sc_at);
     const float blsv = __shfl_sync(0xffffffffu, lsv, i - sc_at);
     const float bisv = __shfl_sync(0xffffffffu, isv, i - sc_at);
-    const uint8_t* st = ring + (i % kStagesR) * C::kStage;
+    const uint8_t* st = ring + drain;
+    drain = drain + C::kStage == kStagesR * C::kStage ? 0 : drain + C::kStage;
     // ---- S = Q K^T: two tiles of 8 keys
     float s[2][4];
 #pragma unroll
