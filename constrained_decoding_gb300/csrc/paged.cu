@@ -872,19 +872,21 @@ __global__ void __launch_bounds__(kWarps * 32, 3) paged_attn_rows_kernel(PagedAt
   }
 }
 
-// Joins the parts of a row, one CTA each: out = sum 2^(M_i - M) O_i / sum
-// 2^(M_i - M) l_i.  With ranges, part i is range i's state of the row; with
-// stretches, the first part is where part_at says and the others begin the
-// stretches of the CTAs after it.  A warp takes 32 parts at a time, one (M, l) to a
-// lane, then their O rows one after the other with the loads in flight
-// together.
+// Joins the parts of a row: out = sum 2^(M_i - M) O_i / sum 2^(M_i - M) l_i.
+// With ranges, part i is range i's state of the row; with stretches, the first
+// part is where part_at says and the others begin the stretches of the CTAs
+// after it.  A warp takes 32 parts at a time, one (M, l) to a lane, then their O
+// rows one after the other with the loads in flight together; W warps share a
+// row (4 where a row may have more than 32 parts, else 1).
 constexpr int kJoinWarps = 4;
-template <int D, class T>
+template <int D, class T, int W>
 __global__ void __launch_bounds__(kJoinWarps * 32) paged_attn_join_kernel(PagedAttnArgs a) {
   griddep_launch_dependents();
   griddep_wait();
   constexpr int kV = D / 32;  // channels of a lane
-  const int row = blockIdx.x;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row = static_cast<int>(blockIdx.x) * (kJoinWarps / W) + warp / W;
+  if (row >= a.q.n_tok * a.Hq) return;
   const int tok = row / a.Hq, hq = row % a.Hq;
   if (tok < a.q.q_off[0] || tok >= a.q.q_off[a.q.n_seq]) return;  // rows of no sequence stay as they are
   int2 at = make_int2(0, a.plan.n_splits);
@@ -899,11 +901,10 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_attn_join_kernel(PagedA
     if (!a.plan.stream) return i * rows + row;
     return static_cast<int64_t>(i == 0 ? at.x : ((at.x >> 5) + i) * 32 + (at.x & 15));
   };
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   float M = -INFINITY, L = 0.f, o[kV];
 #pragma unroll
   for (int k = 0; k < kV; ++k) o[k] = 0.f;
-  for (int i0 = warp * 32; i0 < at.y; i0 += kJoinWarps * 32) {
+  for (int i0 = (warp % W) * 32; i0 < at.y; i0 += W * 32) {
     const int n = min(32, at.y - i0);
     const float2 ml = lane < n ? a.part_ml[part(i0 + lane)] : make_float2(-INFINITY, 0.f);
     float m = ml.y != 0.f ? ml.x : -INFINITY;
@@ -936,24 +937,30 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_attn_join_kernel(PagedA
   if (lane == 0) sml[warp] = make_float2(M, L);
 #pragma unroll
   for (int k = 0; k < kV; ++k) so[warp][lane * kV + k] = o[k];
-  __syncthreads();
-  if (threadIdx.x >= D / 4) return;
-  const int d = threadIdx.x * 4;
+  if (W > 1) __syncthreads();  // the warps of a CTA have one row: they return together or not at all
+  else __syncwarp();
+  if (warp % W || lane >= D / 4) return;
+  const int d = lane * 4;
   RowState st;
 #pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) st.top(sml[w]);
+  for (int w = 0; w < W; ++w) st.top(sml[warp + w]);
 #pragma unroll
-  for (int w = 0; w < kJoinWarps; ++w) st.add(sml[w], *reinterpret_cast<const float4*>(&so[w][d]));
+  for (int w = 0; w < W; ++w) st.add(sml[warp + w], *reinterpret_cast<const float4*>(&so[warp + w][d]));
   finish_row<T>(a, st, tok, hq, d);
 }
 
-template <int D, class T>
-int launch_join(const PagedAttnArgs& a, cudaStream_t s) {
-  auto kern = paged_attn_join_kernel<D, T>;
+template <int D, class T, int W>
+int launch_join_w(const PagedAttnArgs& a, cudaStream_t s) {
+  auto kern = paged_attn_join_kernel<D, T, W>;
   static KernelSetup setup;
   const cudaError_t r = setup.run(kern, 0);
   if (r != cudaSuccess) return r;
-  return launch_k(kern, dim3(static_cast<unsigned>(a.q.n_tok * a.Hq)), dim3(kJoinWarps * 32), 0, s, a);
+  constexpr int kRows = kJoinWarps / W;
+  return launch_k(kern, dim3(static_cast<unsigned>((a.q.n_tok * a.Hq + kRows - 1) / kRows)), dim3(kJoinWarps * 32), 0, s, a);
+}
+template <int D, class T>
+int launch_join(const PagedAttnArgs& a, cudaStream_t s) {
+  return a.plan.parts > 32 ? launch_join_w<D, T, 4>(a, s) : launch_join_w<D, T, 1>(a, s);
 }
 
 template <int D, int FMT, class T>
@@ -1018,6 +1025,8 @@ void plan_paged_attention(int n_tok, int n_seq, int G, int Hkv, int64_t max_kv, 
     want = std::min<int64_t>(sms / tiles, (max_kv + 127) / 128);
   }
   p->n_splits = static_cast<int>(std::max<int64_t>(want, 1));
+  // parts of a row, about: a stretch may cover several items, or an item several stretches
+  p->parts = p->stream ? static_cast<int>(std::min<int64_t>(slots / tiles + 2, 1 << 20)) : p->n_splits;
 }
 
 int launch_paged_attention(const PagedAttnArgs& a, cudaStream_t s) {
