@@ -1004,19 +1004,26 @@ int launch_rows_t(const PagedAttnArgs& a, cudaStream_t s) {
 }  // namespace
 
 void plan_paged_attention(int n_tok, int n_seq, int G, int Hkv, int64_t max_kv, int sms, PagedPlan* p) {
+  max_kv = std::min<int64_t>(max_kv, int64_t{1} << 31);
   const int64_t per = n_seq > 0 ? (n_tok + n_seq - 1) / n_seq : 0;  // query tokens of a sequence, on average
-  p->rows = per * G > 32 ? 256 : 16;
-  const int64_t tiles = std::max<int64_t>(1, n_seq * ((per * G + p->rows - 1) / p->rows) * Hkv);
-  const int64_t slots = static_cast<int64_t>(sms) * 3;  // resident CTAs of the rows kernel
+  const int64_t slots = static_cast<int64_t>(sms) * 3;              // resident CTAs of the rows kernel
+  const auto tiles_of = [&](int64_t rows) { return std::max<int64_t>(1, n_seq * ((per * G + rows - 1) / rows) * Hkv); };
+  // Up to 32 rows a sequence and KV head the rows kernel reads each page at most
+  // twice (64 x 8 k keys, 28 rows: 202 us against 261 in 256-row tiles; 35 rows:
+  // 290 against 262).  Short contexts of few sequences take it further, while
+  // clusters of all their tiles are resident together (901 keys, 144 rows: 12
+  // us against 14.5, and one launch).
+  p->rows = per * G > 32 && (tiles_of(16) * 8 > slots || max_kv > 1024) ? 256 : 16;
+  const int64_t tiles = tiles_of(p->rows);
   p->stream = p->cluster = 0;
   int64_t want;
   if (p->rows == 16) {
     // Ranges for about 7/4 CTAs a slot, at most a cluster's 8; the even
-    // stretches where each is long (over 3000 keys: 64 x 8 k keys take 111 us
-    // against 117 in ranges, 64 x 2 k, 1100 keys each, 51 against 47), or where
+    // stretches where each is long (over 3000 keys: 64 x 8 k keys take 100 us
+    // against 117 in ranges, 64 x 2 k, 1100 keys each, 51 against 45), or where
     // 8 ranges leave most SMs idle and each is longer than the stretches' own
     // 15 us of set-up and joining are worth (1 x 4 k keys: 13 us in a cluster
-    // against 20; 1 x 16 k: 31 against 25).
+    // against 20; 1 x 16 k: 31 against 22).
     want = std::max<int64_t>(1, slots * 7 / 4 / tiles);
     p->stream = n_seq <= 4096 && (tiles * max_kv >= slots * 3000 || (want > 8 && max_kv > 10240));
     want = p->stream ? slots : std::min<int64_t>(std::min<int64_t>(want, 8), (max_kv + 63) / 64);
@@ -1025,8 +1032,8 @@ void plan_paged_attention(int n_tok, int n_seq, int G, int Hkv, int64_t max_kv, 
     want = std::min<int64_t>(sms / tiles, (max_kv + 127) / 128);
   }
   p->n_splits = static_cast<int>(std::max<int64_t>(want, 1));
-  // parts of a row, about: a stretch may cover several items, or an item several stretches
-  p->parts = p->stream ? static_cast<int>(std::min<int64_t>(slots / tiles + 2, 1 << 20)) : p->n_splits;
+  // parts of a row, about: an item may lie on several stretches
+  p->parts = p->stream ? static_cast<int>(slots / tiles + 2) : p->n_splits;
 }
 
 int launch_paged_attention(const PagedAttnArgs& a, cudaStream_t s) {

@@ -29,6 +29,8 @@ def gen(seed):
     (1, 1, 2, 2, False, False), (1, 14, 128, 128, False, False), (3, 5, 80, 32, True, False),
     (7, 3, 64, 62, False, True), (129, 2, 96, 96, True, True), (33, 32, 128, 64, False, False),
     (2, 40, 256, 256, False, True), (513, 1, 16, 16, False, False), (5, 2, 7, 4, True, False), (17, 4, 128, 2, False, False),
+    (9, 3, 40, 24, False, False), (9, 3, 40, 12, True, True), (6, 5, 22, 12, False, True), (6, 9, 22, 6, True, False),
+    (2100, 7, 64, 64, False, False),
 ])
 def test_rope(paged, dtype, n, heads, dim, rot, inter, transpose):
     g = gen(n * 131 + heads)
@@ -196,6 +198,8 @@ def check_append(before, after, scale_before, scale_after, x, x_err, new, lens, 
     ("f16", 32, 64, 3, [31, 32, 33, 100], [1, 31, 32, 33], 0, False, "slot"),
     ("bf16", 16, 128, 2, [70], [3], 126, False, "head"),
     ("f32", 64, 64, 1, [64, 65], [0, 0], 18, True, "head"),
+    ("f16", 16, 64, 6, [2500, 40], [7, 0], 48, False, "head"),     # several heads of a page to a CTA, the last group short
+    ("bf16", 32, 64, 5, [5000], [0], 64, True, "slot"),
 ])
 def test_append(paged, fmt, dtype, page, dim, heads, new, old, rot, inter, order):
     table, kc, vc, ks, vs, k, v, q_off, kv_len, n = append_case(fmt, dtype, page, dim, heads, new, old, rot, inter, order, seed=page + dim)
@@ -452,6 +456,39 @@ def test_attention_rows_behind_the_last_sequence(paged, q_len):
     res, lse = paged.pcd_k_paged_attention(wide[:, 1:7], kc, vc, ks, vs, q_off, kv_len, table, out=out[:, ::2], return_lse=True)
     check_attend(res[:n], lse[:n], R.attention(q, kc, vc, ks, vs, q_off, kv_len, table, True, 0.125))
     assert torch.all(out[:, 1::2] == 3) and torch.all(out[n:] == 3)
+
+
+@pytest.mark.parametrize("q_len", [1, 30, 200])
+def test_attention_unaligned_rows(paged, q_len):
+    """Queries and outputs whose rows start at 2-byte boundaries only."""
+    for dtype in ("f16", "bf16"):
+        q, *rest = attend_case("e4m3", dtype, 32, 128, 6, 2, [q_len, 1], [q_len + 300, 77], 4)
+        flat = torch.zeros(q.numel() + 3, dtype=q.dtype, device="cuda")
+        odd = flat[3:].view(q.shape)
+        odd.copy_(q)
+        out = torch.zeros(q.numel() + 1, dtype=q.dtype, device="cuda")[1:].view(q.shape)
+        got = paged.pcd_k_paged_attention(odd, *rest, out=out)
+        assert got is out and torch.equal(got, paged.pcd_k_paged_attention(q, *rest))
+
+
+def test_two_streams_at_once(paged):
+    """Calls that overlap on two streams, each with its own workspace, and a
+    page that two sequences share for reading."""
+    a = attend_case("int8", "f16", 64, 128, 28, 4, [1] * 6, [20000, 9000, 1, 500, 20000, 64], 2)
+    b = attend_case("e4m3", "bf16", 16, 64, 14, 2, [90, 3], [400, 700], 3)
+    a[-1][4] = a[-1][0]
+    want = [paged.pcd_k_paged_attention(*a), paged.pcd_k_paged_attention(*b)]
+    assert not torch.equal(want[0][0], want[0][4])
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(6):
+        for k, args in enumerate((a, b)):
+            with torch.cuda.stream(streams[k]):
+                got[k].append(paged.pcd_k_paged_attention(*args))
+    torch.cuda.synchronize()
+    for k in range(2):
+        assert all(torch.equal(x, want[k]) for x in got[k])
 
 
 def test_attention_long_cache(paged):
