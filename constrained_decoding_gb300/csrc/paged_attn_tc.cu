@@ -10,10 +10,15 @@
 //   w = exp2(S sk c + log2 sv - M + 8)   one thread a row
 //   O += w V8                  tcgen05.mma, w (fp16) from TMEM over S's columns
 //   l += w / sv                so out = O / l (see the rows kernel)
-// Each K and V block is converted once for both tiles.  The tiles' MMA issuers
-// take turns (P V, then S of the tile's next block): while one tile's rows are
-// in the softmax the tensor cores work for the other.  M moves, and O and l
+// Each K and V block is converted once for both tiles.  M moves, and O and l
 // are rescaled, only when a block exceeds it by 2^7.
+//
+// TMEM's 512 columns at head dim 128: S (then the weights over its first half)
+// and O of both tiles.  The tiles' MMA issuers take turns (P V, then S of the
+// tile's next block, whose columns P V has to free): while one tile's rows are in
+// the softmax the tensor cores work for the other.  At head dim 64 the weights
+// have columns of their own, so S of the next block is made as soon as the
+// softmax holds the present scores, and its threads never wait for the MMAs.
 //
 // Registers: 512 threads launch with 128 each; the two softmax warpgroups
 // hold a row of 128 scores and take 192, paid for by the other two (64 each):
@@ -50,6 +55,8 @@ struct TileCfg {
   static constexpr int kOffWhole = kOffSc + 4 * 8 * 16;  // [4]: is every key of the block there?
   static constexpr int kOffBar = kOffWhole + 16;
   static constexpr int kSmem = kOffBar + 256 + 1024;    // + alignment slack
+  static constexpr bool kOwnP = D == 64;                // the weights' columns: their own, or S's
+  static constexpr int kColO = 2 * kBlock, kColP = kOwnP ? kColO + 2 * D : 0, kStepP = kOwnP ? kBlock / 2 : kBlock;
   static_assert(kSmem <= 227 * 1024, "shared memory of a CTA");
 };
 
@@ -66,7 +73,17 @@ __device__ __forceinline__ void tmem_ld_32cols_async(uint32_t taddr, float* v) {
         "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(taddr));
 }
-__device__ __forceinline__ void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// Waits for the loads issued so far; 32 of their values pass through, so that
+// nothing uses them before.
+__device__ __forceinline__ void tmem_ld_wait32(float* v) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+f"(v[0]), "+f"(v[1]), "+f"(v[2]), "+f"(v[3]), "+f"(v[4]), "+f"(v[5]), "+f"(v[6]), "+f"(v[7]),
+                 "+f"(v[8]), "+f"(v[9]), "+f"(v[10]), "+f"(v[11]), "+f"(v[12]), "+f"(v[13]), "+f"(v[14]), "+f"(v[15]),
+                 "+f"(v[16]), "+f"(v[17]), "+f"(v[18]), "+f"(v[19]), "+f"(v[20]), "+f"(v[21]), "+f"(v[22]), "+f"(v[23]),
+                 "+f"(v[24]), "+f"(v[25]), "+f"(v[26]), "+f"(v[27]), "+f"(v[28]), "+f"(v[29]), "+f"(v[30]), "+f"(v[31])
+               :
+               : "memory");
+}
 // 16 columns, without waiting.
 __device__ __forceinline__ void tmem_st_16cols_async(uint32_t taddr, const uint32_t* v) {
   asm volatile(
@@ -119,7 +136,8 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
   uint64_t* raw_free = bars + 18;  // [K, V] codes converted
   uint64_t* turn = bars + 20;    // [tile] its issuer's turn
   uint64_t* drain = bars + 22;   // [tile] its issuer's MMAs are done
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 24);
+  uint64_t* s_free = bars + 24;  // [tile] scores are in the softmax's registers (weights with columns of their own)
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 26);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   float4* sc = reinterpret_cast<float4*>(smem + C::kOffSc);
   volatile int* whole_block = reinterpret_cast<volatile int*>(smem + C::kOffWhole);
@@ -165,6 +183,7 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
       mbar_init(&q_full[s], 4);
       mbar_init(&raw_full[s], 1);
       mbar_init(&turn[s], 1);
+      mbar_init(&s_free[s], 4);
       mbar_init(&drain[s], 1);
       mbar_init(&raw_free[s], 4);
     }
@@ -180,7 +199,6 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tbase = *tmem_slot;
-  const uint32_t col_o = 2 * kBlock;
   auto fail = [&](int code) {
     record_error(a.err, code);
     *abort_flag = 1;
@@ -193,15 +211,13 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
     regs_down<64>();
     if ((warp == 0 || (warp == 2 && two)) && nb > 0) {
       // ------------------------------------------------------------ MMA issuers, one a tile
-      // They take turns: P V of the tile and S of its next block, then the other
-      // tile, so that one tile's softmax runs under the other's products, and
-      // one's commits under the other's MMAs.  A warp stays together and one lane
-      // issues, so that descriptors are computed in uniform registers.
+      // A warp stays together and one lane issues, so that descriptors are
+      // computed in uniform registers (a lone lane took 20 more clocks an MMA).
       constexpr uint32_t kIdS = idesc_f16_f32(kTile, kBlock);
       constexpr uint32_t kIdO = idesc_f16_f32(kTile, D) | (1u << 16);  // B (V) is MN-major
       const int t = __shfl_sync(0xffffffffu, warp >> 1, 0);
       const uint32_t tb = __shfl_sync(0xffffffffu, tbase, 0);
-      const uint32_t dS = tb + t * kBlock, dO = tb + col_o + t * D;
+      const uint32_t dS = tb + t * kBlock, dO = tb + C::kColO + t * D;
       const uint64_t dq = sdesc_kmajor_sw128(smem_u32(smem + t * C::kOp)), dk = sdesc_kmajor_sw128(smem_u32(smem + C::kOffK));
       const uint64_t dv = sdesc_mnmajor_sw128(smem_u32(smem + C::kOffV), kHalf, 1024);
       auto issue_s = [&](int st) {
@@ -213,7 +229,7 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
             const uint32_t o = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
             umma_f16(dS, dq + o, k0 + o, kIdS, k > 0 ? 1u : 0u);
           }
-          if (two) mbar_arrive(&turn[t ^ 1]);
+          if (two && !C::kOwnP) mbar_arrive(&turn[t ^ 1]);
           umma_commit(&s_full[t]);
           mbar_arrive(&s_full[t]);  // orders the constants, which the commit alone would not
           umma_commit(&k_free[st]);
@@ -222,14 +238,24 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
       };
       // turn[t] completes once before each of the tile's turns; the first tile's first turn is free
       bool ok = mbar_wait(&k_full[0], 0, kWaitNs) && mbar_wait(&q_full[t], 0, kWaitNs) &&
-                (t == 0 || mbar_wait(&turn[1], 0, kWaitNs));
+                (t == 0 || C::kOwnP || mbar_wait(&turn[1], 0, kWaitNs));
       ok = __all_sync(0xffffffffu, ok);
       if (ok) issue_s(0);
+      const uint32_t dP = C::kOwnP ? tb + C::kColP + t * C::kStepP : dS;
       for (int i = 0; ok && i < nb; ++i) {
         const int st = i & 1;
+        const uint32_t par = static_cast<uint32_t>(i & 1);
+        auto next_s = [&](uint64_t* freed) {
+          if (i + 1 >= nb) return;
+          ok = mbar_wait(&k_full[st ^ 1], static_cast<uint32_t>(((i + 1) >> 1) & 1), kWaitNs) && mbar_wait(freed, par, kWaitNs);
+          ok = __all_sync(0xffffffffu, ok && !*abort_flag);
+          if (ok) issue_s(st ^ 1);
+        };
+        if (C::kOwnP) next_s(&s_free[t]);
+        if (!ok) break;
         ok = mbar_wait(&v_full[st], static_cast<uint32_t>((i >> 1) & 1), kWaitNs) &&
-             (!two || mbar_wait(&turn[t], static_cast<uint32_t>((i + t) & 1), kWaitNs)) &&
-             mbar_wait(&p_full[t], static_cast<uint32_t>(i & 1), kWaitNs);
+             (!two || C::kOwnP || mbar_wait(&turn[t], static_cast<uint32_t>((i + t) & 1), kWaitNs)) &&
+             mbar_wait(&p_full[t], par, kWaitNs);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after_sync();
@@ -238,19 +264,13 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
         if (elect_one_sync()) {
 #pragma unroll
           for (int k = 0; k < kBlock / 16; ++k)
-            umma_f16_ts(dO, dS + k * 8, v + k * (16 * 128 >> 4), kIdO, k > 0 ? 1u : acc);
+            umma_f16_ts(dO, dP + k * 8, v + k * (16 * 128 >> 4), kIdO, k > 0 ? 1u : acc);
           umma_commit(&pv_done[t]);
           umma_commit(&v_free[st]);
-          if (two && i + 1 == nb) mbar_arrive(&turn[t ^ 1]);
+          if (two && !C::kOwnP && i + 1 == nb) mbar_arrive(&turn[t ^ 1]);
         }
         __syncwarp();
-        if (i + 1 < nb) {
-          // S takes the columns that P V reads its weights from
-          ok = mbar_wait(&k_full[st ^ 1], static_cast<uint32_t>(((i + 1) >> 1) & 1), kWaitNs) &&
-               mbar_wait(&pv_done[t], static_cast<uint32_t>(i & 1), kWaitNs);
-          ok = __all_sync(0xffffffffu, ok && !*abort_flag);
-          if (ok) issue_s(st ^ 1);
-        }
+        if (!C::kOwnP) next_s(&pv_done[t]);  // S takes the columns that P V reads its weights from
       }
       if (!ok && lane == 0) fail(DEV_WAIT_TIMEOUT_MMA);
       if (elect_one_sync()) {
@@ -289,8 +309,8 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
             const int cid = __shfl_sync(0xffffffffu, good ? id : -1, pl & 31);
             const bool there = cid >= 0 && j0 + lane * 16 < len;
             const uint32_t all = __ballot_sync(0xffffffffu, there) & 0xffu;
-            // block i - 4 has left the softmax: K of block i - 1 was converted, for which every S of block i - 3
-            // was done, each of which came after the P V of block i - 4
+            // block i - 4 has left the softmax: K of block i - 1 was converted, after V of block i - 2, for which
+            // the P V of block i - 4 were done
             if (lane < kBlock / 16) {
               float4 c = make_float4(0.f, 0.f, 0.f, 0.f);
               if (there) {
@@ -384,7 +404,7 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
     const int tok = it.row0 + rr / a.G, hq = hk * a.G + rr % a.G;
     const int vis = seen(rr);
     const uint32_t trow = tbase + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
-    const uint32_t ts = trow + t * kBlock, to = trow + col_o + t * D;
+    const uint32_t ts = trow + t * kBlock, tp = C::kOwnP ? trow + C::kColP + t * C::kStepP : ts, to = trow + C::kColO + t * D;
     float m_ref = -INFINITY, l = 0.f, qs = 0.f;
     bool ok = active;
     if (active && nb > 0) {
@@ -447,7 +467,13 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld_32cols_async(ts + 32 * c, s + 32 * c);
         const float4* cs = sc + (i & 3) * 8;
-        tmem_ld_wait();
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld_wait32(s + 32 * c);
+        if (C::kOwnP) {
+          tc_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&s_free[t]);
+        }
         const int j0 = (b0 + i) * kBlock;
         const bool plain = whole_block[i & 3] != 0 && j0 + kBlock <= wmin;
         float mx = -INFINITY;
@@ -486,18 +512,14 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
             if (!ok) break;
             tc_fence_after_sync();
 #pragma unroll 1
-            for (int c = 0; c < D / 16; ++c) {
-              uint32_t o[16];
-              asm volatile(
-                  "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-                  "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-                  : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]), "=r"(o[7]),
-                    "=r"(o[8]), "=r"(o[9]), "=r"(o[10]), "=r"(o[11]), "=r"(o[12]), "=r"(o[13]), "=r"(o[14]), "=r"(o[15])
-                  : "r"(to + 16 * c));
-              tmem_ld_wait();
+            for (int c = 0; c < D / 32; ++c) {
+              float o[32];
+              tmem_ld_32cols_async(to + 32 * c, o);
+              tmem_ld_wait32(o);
 #pragma unroll
-              for (int x = 0; x < 16; ++x) o[x] = __float_as_uint(__uint_as_float(o[x]) * f);
-              tmem_st_16cols_async(to + 16 * c, o);
+              for (int x = 0; x < 32; ++x) o[x] *= f;
+              tmem_st_16cols_async(to + 32 * c, reinterpret_cast<const uint32_t*>(o));
+              tmem_st_16cols_async(to + 32 * c + 16, reinterpret_cast<const uint32_t*>(o) + 16);
             }
             tmem_st_wait();
           }
@@ -525,8 +547,13 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
             // a poisoned scale (NaN) counts only for rows that see its keys
             l = fmaf(sum.x + sum.y, plain || vis > j0 + 16 * g ? k.z : 0.f, l);
           }
-          tmem_st_16cols_async(ts + 16 * q2, w);
+          if (C::kOwnP && q2 == 0 && i > 0) {  // the block before has left the weights' columns
+            ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[t], static_cast<uint32_t>((i - 1) & 1), kWaitNs));
+            tc_fence_after_sync();
+          }
+          tmem_st_16cols_async(tp + 16 * q2, w);
         }
+        if (!ok) break;
         tmem_st_wait();
         tc_fence_before_sync();
         __syncwarp();
@@ -561,7 +588,7 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
           const int d = p * (split ? kRowB / 4 : kRowB / 2) + 32 * c;
           if (have) {
             tmem_ld_32cols_async(to + d, o);
-            tmem_ld_wait();
+            tmem_ld_wait32(o);
           }
           const bool some = have && l != 0.f;
           if (split) {
