@@ -398,8 +398,8 @@ int launch_kv_append(const AppendArgs& a, int sms, cudaStream_t s) {
 
 namespace {
 // =================================================================== attention
-// Few query rows (16 to a tile: tokens x the G query heads of one KV head),
-// warp tensor-core MMA.
+// Few query rows (8 or 16 to a tile: tokens x the G query heads of one KV
+// head), warp tensor-core MMA.
 //
 // Every warp walks its own 16-key blocks of the tile's key range with a
 // private cp.async ring, so no barrier stands in the key loop.  Codes become
@@ -416,6 +416,12 @@ namespace {
 // order), and a V fragment's column is any channel, so a lane reads 16
 // consecutive channels of its four keys and pairs keys by byte permutes: no
 // ldmatrix, no transposition in shared memory.
+//
+// Tiles of 16 rows compute S = Q K^T and O = w V with the rows as the MMA's 16.
+// Tiles of 8 compute the transposes, K Q^T and V^T w^T, with keys and channels as
+// the 16 and the rows as the 8: half the MMAs; the weights change sides by a
+// register transpose (64 x 8 k keys of 7 query heads: 89 us against 99; 300
+// contexts of up to 600: 43 against 53).
 //
 // How the work is cut: small calls give every item (a tile of one KV head) to a
 // thread-block cluster of up to 8 CTAs that divide its keys and join through
@@ -438,8 +444,9 @@ struct RowsCfg {
 
 // A sequence as the rows kernel divides it.
 struct RowsSeq {
-  int row0, n, len, tiles, blocks;  // tiles of 16 rows (0: nothing to do), 16-key blocks of an item
+  int row0, n, len, tiles, blocks;  // tiles of rows (0: nothing to do), 16-key blocks of an item
 };
+template <int ROWS>
 __device__ __forceinline__ RowsSeq rows_seq(const PagedAttnArgs& a, int row0, int n, int len) {
   RowsSeq q{row0, n, len, 0, 1};
   if (n == 0) return q;
@@ -447,7 +454,7 @@ __device__ __forceinline__ RowsSeq rows_seq(const PagedAttnArgs& a, int row0, in
     record_error(a.err, DEV_BAD_INDEX);
     return q;
   }
-  q.tiles = (n * a.G + 15) >> 4;
+  q.tiles = (n * a.G + ROWS - 1) / ROWS;
   if (len < 0 || len > kMaxLen || len > static_cast<int64_t>(a.q.table_stride) << a.c.page_log2) {
     record_error(a.err, DEV_BAD_INDEX);
     q.len = 0;
@@ -455,15 +462,16 @@ __device__ __forceinline__ RowsSeq rows_seq(const PagedAttnArgs& a, int row0, in
   q.blocks = max(1, (q.len + 15) >> 4);  // an item without keys still writes its rows
   return q;
 }
+template <int ROWS>
 __device__ __forceinline__ RowsSeq rows_seq(const PagedAttnArgs& a, int s) {
   const int row0 = a.q.q_off[s];
-  return rows_seq(a, row0, static_cast<int>(static_cast<unsigned>(a.q.q_off[s + 1]) - static_cast<unsigned>(row0)), a.q.kv_len[s]);
+  return rows_seq<ROWS>(a, row0, static_cast<int>(static_cast<unsigned>(a.q.q_off[s + 1]) - static_cast<unsigned>(row0)), a.q.kv_len[s]);
 }
 __device__ __forceinline__ int64_t rows_units(const PagedAttnArgs& a, const RowsSeq& q) {
   return static_cast<int64_t>(q.tiles) * a.c.Hkv * q.blocks;
 }
 
-template <int D, int FMT, class T>
+template <int D, int FMT, class T, int ROWS>
 __global__ void __launch_bounds__(kWarps * 32, 3) paged_attn_rows_kernel(PagedAttnArgs a) {
   using C = RowsCfg<D>;
   extern __shared__ __align__(128) uint8_t smem[];
@@ -479,7 +487,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) paged_attn_rows_kernel(PagedAt
   if (stream) {
     for (int s0 = 0; s0 < a.q.n_seq; s0 += 32) {
       int64_t w = 0;
-      if (s0 + lane < a.q.n_seq) w = rows_units(a, rows_seq(a, s0 + lane));
+      if (s0 + lane < a.q.n_seq) w = rows_units(a, rows_seq<ROWS>(a, s0 + lane));
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
       line += w;
@@ -490,7 +498,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) paged_attn_rows_kernel(PagedAt
     u_end = line * (blockIdx.x + 1) / n_cta;
     for (int s0 = 0;; s0 += 32) {
       int64_t w = 0;
-      if (s0 + lane < a.q.n_seq) w = rows_units(a, rows_seq(a, s0 + lane));
+      if (s0 + lane < a.q.n_seq) w = rows_units(a, rows_seq<ROWS>(a, s0 + lane));
       int64_t upto = w;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -506,14 +514,14 @@ __global__ void __launch_bounds__(kWarps * 32, 3) paged_attn_rows_kernel(PagedAt
       }
       before += __shfl_sync(0xffffffffu, upto, 31);
     }
-    sq = rows_seq(a, seq);
+    sq = rows_seq<ROWS>(a, seq);
   } else {
     // (what returns here returns in every CTA of a cluster)
-    const SeqItem it = find_item(a.q, static_cast<int>(blockIdx.x), a.G, 4, 1);
+    const SeqItem it = find_item(a.q, static_cast<int>(blockIdx.x), a.G, ROWS == 8 ? 3 : 4, 1);
     if (it.seq < 0) return;
     seq = it.seq;
     tile = it.local;
-    sq = rows_seq(a, it.row0, it.n, it.len);
+    sq = rows_seq<ROWS>(a, it.row0, it.n, it.len);
     if (tile >= sq.tiles) return;
   }
   for (;;) {
@@ -521,7 +529,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) paged_attn_rows_kernel(PagedAt
   if (stream) {
     while (u >= before + rows_units(a, sq)) {
       before += rows_units(a, sq);
-      sq = rows_seq(a, ++seq);
+      sq = rows_seq<ROWS>(a, ++seq);
     }
     const int64_t at = u - before;
     const int64_t item = at / sq.blocks;
@@ -533,9 +541,9 @@ __global__ void __launch_bounds__(kWarps * 32, 3) paged_attn_rows_kernel(PagedAt
   }
   const int n = sq.n, len = sq.len;
   const int R = n * a.G;
-  const int r0 = tile * 16;
-  const int r_end = min(r0 + 16, R);
-  const bool upper = r_end - r0 > 8;  // rows 8 .. 15 exist
+  const int r0 = tile * ROWS;
+  const int r_end = min(r0 + ROWS, R);
+  const bool upper = ROWS == 16 && r_end - r0 > 8;  // rows 8 .. 15 exist
   // keys seen by a row: all, or up to its own position
   const int first = a.causal ? len - n + 1 : len;  // by the sequence's first token
   auto seen = [&](int r) { return a.causal ? first + min(r, R - 1) / a.G : len; };
@@ -627,12 +635,14 @@ __global__ void __launch_bounds__(kWarps * 32, 3) paged_attn_rows_kernel(PagedAt
   int sc_at = 0, drain = 0;
 
   // ---- Q fragments: k-step t takes channels (64 * (t / 4) + 16 c + 4 (t % 4)) + {0, 1 | 2, 3}
-  uint32_t qf[D / 16][4];
-  float qs[2];
-  float row_m[2] = {-INFINITY, -INFINITY}, row_l[2] = {0.f, 0.f};
+  // Row g of the tile, and row g + 8: rows of MMA's A, or (8 rows) the columns of its B, two registers a step
+  constexpr int kE = ROWS / 8;
+  uint32_t qf[D / 16][2 * kE];
+  float qs[2] = {0.f, 0.f};
+  float row_m[2] = {-INFINITY, -INFINITY}, row_l[2] = {0.f, 0.f};  // of rows g, g + 8; or 2c, 2c + 1
   int vis[2];
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
+  for (int e = 0; e < kE; ++e) {
     const int r = r0 + g + 8 * e;
     vis[e] = seen(r);
     const bool ok = r < R;
@@ -668,17 +678,27 @@ __global__ void __launch_bounds__(kWarps * 32, 3) paged_attn_rows_kernel(PagedAt
     for (int t = 0; t < D / 16; ++t) {
       if (std::is_same<T, __half>::value) {
         qf[t][e] = reinterpret_cast<const uint32_t*>(v[t])[0];
-        qf[t][2 + e] = reinterpret_cast<const uint32_t*>(v[t])[1];
+        qf[t][kE + e] = reinterpret_cast<const uint32_t*>(v[t])[1];
       } else {
         qf[t][e] = pack2(to_f(v[t][0]) * down, to_f(v[t][1]) * down);
-        qf[t][2 + e] = pack2(to_f(v[t][2]) * down, to_f(v[t][3]) * down);
+        qf[t][kE + e] = pack2(to_f(v[t][2]) * down, to_f(v[t][3]) * down);
       }
     }
   }
 
-  float o[D / 8][4];
+  if (ROWS == 8) {  // the softmax's lanes have rows 2c and 2c + 1
+    const float q = qs[0];
 #pragma unroll
-  for (int t = 0; t < D / 8; ++t)
+    for (int e = 0; e < 2; ++e) {
+      qs[e] = __shfl_sync(0xffffffffu, q, (2 * c + e) * 4);
+      vis[e] = seen(r0 + 2 * c + e);
+    }
+  }
+
+  constexpr int kO = ROWS == 8 ? D / 16 : D / 8;
+  float o[kO][4];
+#pragma unroll
+  for (int t = 0; t < kO; ++t)
 #pragma unroll
     for (int i = 0; i < 4; ++i) o[t][i] = 0.f;
 
@@ -696,13 +716,14 @@ __global__ void __launch_bounds__(kWarps * 32, 3) paged_attn_rows_kernel(PagedAt
     const float bisv = __shfl_sync(0xffffffffu, isv, i - sc_at);
     const uint8_t* st = ring + drain;
     drain = drain + C::kStage == kStagesR * C::kStage ? 0 : drain + C::kStage;
-    // ---- S = Q K^T: two tiles of 8 keys
+    // ---- S = Q K^T: two tiles of 8 keys (or K Q^T: 16 keys by 8 rows)
     float s[2][4];
 #pragma unroll
     for (int t = 0; t < 2; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
 #pragma unroll
     for (int hf = 0; hf < D / 64; ++hf) {
       uint4 w[2];
+      uint32_t ka[2][2];
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
         const int key = 8 * t + g;
@@ -714,12 +735,62 @@ __global__ void __launch_bounds__(kWarps * 32, 3) paged_attn_rows_kernel(PagedAt
         for (int t = 0; t < 2; ++t) {
           uint32_t h0, h1;
           codes4_half<FMT>(q == 0 ? w[t].x : q == 1 ? w[t].y : q == 2 ? w[t].z : w[t].w, &h0, &h1);
-          mma16816(s[t], qf[4 * hf + q], h0, h1);
+          if constexpr (ROWS == 16) mma16816(s[t], qf[4 * hf + q], h0, h1);
+          else ka[t][0] = h0, ka[t][1] = h1;
+          if (ROWS == 8 && t == 1) {  // two chains of steps, joined below
+            const uint32_t kf[4] = {ka[0][0], h0, ka[0][1], h1};
+            mma16816(s[q & 1], kf, qf[4 * hf + q][0], qf[4 * hf + q][1]);
+          }
         }
     }
     // ---- weights (rows 8 .. 15 only where the tile has them)
     const int j0 = block_at(i) << 4;
     uint32_t pf[4];
+    if constexpr (ROWS == 8) {
+      // x[e]: keys g and g + 8 of row 2c + e
+      float x[2][2], iv[2];
+      const bool edge = j0 + 16 > kmin || bisv == 0.f;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float ak = qs[e] * bsk;
+        x[e][0] = fmaf(s[0][e] + s[1][e], ak, blsv);
+        x[e][1] = fmaf(s[0][2 + e] + s[1][2 + e], ak, blsv);
+        iv[e] = bisv;
+        if (edge) {
+          const int lim = bisv == 0.f ? 0 : vis[e] - j0 - g;
+          x[e][0] = 0 < lim ? x[e][0] : -INFINITY;
+          x[e][1] = 8 < lim ? x[e][1] : -INFINITY;
+          if (vis[e] <= j0) iv[e] = 0.f;  // a poisoned scale (NaN) counts only for rows that see its keys
+        }
+      }
+      const float m0 = fmaxf(x[0][0], x[0][1]), m1 = fmaxf(x[1][0], x[1][1]);
+      if (__any_sync(0xffffffffu, m0 > row_m[0] + kSlack || m1 > row_m[1] + kSlack)) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float m = e ? m1 : m0;
+#pragma unroll
+          for (int w = 4; w < 32; w <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, w));
+          m = fmaxf(m, row_m[e]);
+          const float f = row_m[e] == -INFINITY ? 0.f : ex2_approx(row_m[e] - m);
+          row_m[e] = m;
+          row_l[e] *= f;
+#pragma unroll
+          for (int t = 0; t < kO; ++t) {
+            o[t][e] *= f;
+            o[t][2 + e] *= f;
+          }
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float mb = (row_m[e] == -INFINITY ? 0.f : row_m[e]) - kBias;
+        x[e][0] = ex2_approx(x[e][0] - mb);
+        x[e][1] = ex2_approx(x[e][1] - mb);
+        row_l[e] = fmaf(x[e][0] + x[e][1], iv[e], row_l[e]);
+      }
+      pf[0] = transpose8x8(pack2(x[0][0], x[1][0]));  // rows by keys 0 .. 7
+      pf[1] = transpose8x8(pack2(x[0][1], x[1][1]));  // ... 8 .. 15
+    } else {
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
       if (e == 1 && !upper) {
@@ -748,7 +819,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) paged_attn_rows_kernel(PagedAt
         row_m[e] = m;
         row_l[e] *= f;
 #pragma unroll
-        for (int t = 0; t < D / 8; ++t) {
+        for (int t = 0; t < kO; ++t) {
           o[t][2 * e] *= f;
           o[t][2 * e + 1] *= f;
         }
@@ -759,6 +830,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) paged_attn_rows_kernel(PagedAt
       row_l[e] = fmaf((x[0] + x[1]) + (x[2] + x[3]), iv, row_l[e]);
       pf[e] = pack2(x[0], x[1]);
       pf[2 + e] = pack2(x[2], x[3]);
+    }
     }
     // ---- O += w V: column tile t's lane group g is channel g * (D / 8) + t
     const uint8_t* sv = st + 16 * D;
@@ -782,32 +854,42 @@ __global__ void __launch_bounds__(kWarps * 32, 3) paged_attn_rows_kernel(PagedAt
       uint32_t v0[2], v1[2];
       codes_cross_half<FMT>(vr[0][t >> 2], vr[1][t >> 2], (t >> 1) & 1, &v0[0], &v0[1]);
       codes_cross_half<FMT>(vr[2][t >> 2], vr[3][t >> 2], (t >> 1) & 1, &v1[0], &v1[1]);
-      mma16816(o[t], pf, v0[0], v1[0]);
-      mma16816(o[t + 1], pf, v0[1], v1[1]);
+      if constexpr (ROWS == 16) {
+        mma16816(o[t], pf, v0[0], v1[0]);
+        mma16816(o[t + 1], pf, v0[1], v1[1]);
+      } else {  // channels g * (D / 8) + t and + 1 of all lane groups as the MMA's rows g and g + 8
+        const uint32_t vf[4] = {v0[0], v0[1], v1[0], v1[1]};
+        mma16816(o[t / 2], vf, pf[0], pf[1]);
+      }
     }
     __syncwarp();
   }
   cp_async_wait<0>();
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    row_l[e] += __shfl_xor_sync(0xffffffffu, row_l[e], 1);
-    row_l[e] += __shfl_xor_sync(0xffffffffu, row_l[e], 2);
-  }
+  for (int e = 0; e < 2; ++e)
+#pragma unroll
+    for (int w = ROWS == 8 ? 4 : 1; w < (ROWS == 8 ? 32 : 4); w <<= 1) row_l[e] += __shfl_xor_sync(0xffffffffu, row_l[e], w);
   // ---- join the warps
   __syncthreads();
   float* red = reinterpret_cast<float*>(smem);
   float2* ml = reinterpret_cast<float2*>(smem + C::kRedMl);
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
-    if (e == 1 && !upper) break;
-    const int r = g + 8 * e;
-    if (c == 0) ml[warp * 16 + r] = make_float2(row_m[e], row_l[e]);
+    if (ROWS == 16 && e == 1 && !upper) break;
+    const int r = ROWS == 8 ? 2 * c + e : g + 8 * e;
+    if ((ROWS == 8 ? g : c) == 0) ml[warp * 16 + r] = make_float2(row_m[e], row_l[e]);
 #pragma unroll
-    for (int t = 0; t < D / 8; t += 2)  // accumulator column 2c + i is lane group 2c + i's channel
+    for (int t = 0; t < D / 8; t += 2) {
+      if constexpr (ROWS == 8) {
+        *reinterpret_cast<float2*>(&red[(warp * 16 + r) * C::kRedLd + g * (D / 8) + t]) =
+            make_float2(o[t / 2][e], o[t / 2][2 + e]);
+      } else {  // accumulator column 2c + i is lane group 2c + i's channel
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        *reinterpret_cast<float2*>(&red[(warp * 16 + r) * C::kRedLd + (2 * c + i) * (D / 8) + t]) =
-            make_float2(o[t][2 * e + i], o[t + 1][2 * e + i]);
+        for (int i = 0; i < 2; ++i)
+          *reinterpret_cast<float2*>(&red[(warp * 16 + r) * C::kRedLd + (2 * c + i) * (D / 8) + t]) =
+              make_float2(o[t][2 * e + i], o[t + 1][2 * e + i]);
+      }
+    }
   }
   __syncthreads();
   const bool cluster = a.plan.cluster != 0;
@@ -963,16 +1045,16 @@ int launch_join(const PagedAttnArgs& a, cudaStream_t s) {
   return a.plan.parts > 32 ? launch_join_w<D, T, 4>(a, s) : launch_join_w<D, T, 1>(a, s);
 }
 
-template <int D, int FMT, class T>
+template <int D, int FMT, class T, int ROWS>
 int launch_rows(const PagedAttnArgs& a, cudaStream_t s) {
   using C = RowsCfg<D>;
-  auto kern = paged_attn_rows_kernel<D, FMT, T>;
+  auto kern = paged_attn_rows_kernel<D, FMT, T, ROWS>;
   static KernelSetup setup;
   const cudaError_t r = setup.run(kern, C::kSmem);
   if (r != cudaSuccess) return r;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = a.plan.stream ? dim3(static_cast<unsigned>(a.plan.n_splits))
-                              : dim3(static_cast<unsigned>(((static_cast<int64_t>(a.q.n_tok) * a.G) >> 4) + a.q.n_seq),
+                              : dim3(static_cast<unsigned>(((static_cast<int64_t>(a.q.n_tok) * a.G) / ROWS) + a.q.n_seq),
                                      static_cast<unsigned>(a.c.Hkv), static_cast<unsigned>(a.plan.n_splits));
   cfg.blockDim = dim3(kWarps * 32);
   cfg.dynamicSmemBytes = C::kSmem;
@@ -998,7 +1080,9 @@ int launch_rows(const PagedAttnArgs& a, cudaStream_t s) {
 
 template <int D, int FMT>
 int launch_rows_t(const PagedAttnArgs& a, cudaStream_t s) {
-  return a.dtype == PCD_DTYPE_BF16 ? launch_rows<D, FMT, __nv_bfloat16>(a, s) : launch_rows<D, FMT, __half>(a, s);
+  if (a.plan.rows == 8)
+    return a.dtype == PCD_DTYPE_BF16 ? launch_rows<D, FMT, __nv_bfloat16, 8>(a, s) : launch_rows<D, FMT, __half, 8>(a, s);
+  return a.dtype == PCD_DTYPE_BF16 ? launch_rows<D, FMT, __nv_bfloat16, 16>(a, s) : launch_rows<D, FMT, __half, 16>(a, s);
 }
 
 }  // namespace
@@ -1006,26 +1090,27 @@ int launch_rows_t(const PagedAttnArgs& a, cudaStream_t s) {
 void plan_paged_attention(int n_tok, int n_seq, int G, int Hkv, int64_t max_kv, int sms, PagedPlan* p) {
   max_kv = std::min<int64_t>(max_kv, int64_t{1} << 31);
   const int64_t per = n_seq > 0 ? (n_tok + n_seq - 1) / n_seq : 0;  // query tokens of a sequence, on average
-  const int64_t slots = static_cast<int64_t>(sms) * 3;              // resident CTAs of the rows kernel
   const auto tiles_of = [&](int64_t rows) { return std::max<int64_t>(1, n_seq * ((per * G + rows - 1) / rows) * Hkv); };
   // Up to 32 rows a sequence and KV head the rows kernel reads each page at most
   // twice (64 x 8 k keys, 28 rows: 202 us against 261 in 256-row tiles; 35 rows:
   // 290 against 262).  Short contexts of few sequences take it further, while
   // clusters of all their tiles are resident together (901 keys, 144 rows: 12
   // us against 14.5, and one launch).
-  p->rows = per * G > 32 && (tiles_of(16) * 8 > slots || max_kv > 1024) ? 256 : 16;
+  p->rows = per * G <= 8 ? 8 : per * G > 32 && (tiles_of(16) * 8 > 3 * sms || max_kv > 1024) ? 256 : 16;
   const int64_t tiles = tiles_of(p->rows);
+  const int64_t slots = static_cast<int64_t>(sms) * 3;  // resident CTAs of the rows kernel
   p->stream = p->cluster = 0;
   int64_t want;
-  if (p->rows == 16) {
-    // Ranges for about 7/4 CTAs a slot, at most a cluster's 8; the even
-    // stretches where each is long (over 3000 keys: 64 x 8 k keys take 100 us
-    // against 117 in ranges, 64 x 2 k, 1100 keys each, 51 against 45), or where
-    // 8 ranges leave most SMs idle and each is longer than the stretches' own
-    // 15 us of set-up and joining are worth (1 x 4 k keys: 13 us in a cluster
-    // against 20; 1 x 16 k: 31 against 22).
+  if (p->rows <= 16) {
+    // Ranges for about 7/4 CTAs a slot, at most a cluster's 8.  The even
+    // stretches where there is much to read in long contexts (four KV heads, 7
+    // query heads each: 64 x 8 k keys take 89 us against 101 in ranges, 16 x 8 k
+    // 35 against 41, 64 x 1 k .. 2 k 35 against 37, but 300 x 300 .. 600 58
+    // against 44), or where 8 ranges leave most SMs idle and each is longer than
+    // the stretches' own 17 us of set-up and joining are worth (1 x 8 k keys: 15
+    // us in a cluster against 18.5; 1 x 16 k: 24 against 19.5).
     want = std::max<int64_t>(1, slots * 7 / 4 / tiles);
-    p->stream = n_seq <= 4096 && (tiles * max_kv >= slots * 3000 || (want > 8 && max_kv > 10240));
+    p->stream = n_seq <= 4096 && ((max_kv >= 2000 && tiles * max_kv >= slots * 1000) || (want > 8 && max_kv > 10240));
     want = p->stream ? slots : std::min<int64_t>(std::min<int64_t>(want, 8), (max_kv + 63) / 64);
     p->cluster = !p->stream && want > 1;
   } else {

@@ -58,8 +58,8 @@ struct AppendArgs {
 };
 int launch_kv_append(const AppendArgs& a, int sms, cudaStream_t s);
 
-// How a call is cut up.  rows: query rows of a work item (16: warp MMA, 256:
-// tcgen05).  n_splits: ranges that every item's keys are divided into, walked
+// How a call is cut up.  rows: query rows of a work item (8 or 16: warp MMA,
+// 256: tcgen05).  n_splits: ranges that every item's keys are divided into, walked
 // by a thread-block cluster that joins them (cluster) or joined by a second
 // kernel; with stream, CTAs that share the blocks of all items evenly.  parts:
 // of a row for that kernel, as far as the host knows.
