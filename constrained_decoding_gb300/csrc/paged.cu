@@ -1092,14 +1092,15 @@ void plan_paged_attention(int n_tok, int n_seq, int G, int Hkv, int64_t max_kv, 
   const int64_t per = n_seq > 0 ? (n_tok + n_seq - 1) / n_seq : 0;  // query tokens of a sequence, on average
   const auto tiles_of = [&](int64_t rows) { return std::max<int64_t>(1, n_seq * ((per * G + rows - 1) / rows) * Hkv); };
   // Up to 32 rows a sequence and KV head the rows kernel reads each page at most
-  // twice (64 x 8 k keys, 28 rows: 202 us against 261 in 256-row tiles; 35 rows:
-  // 290 against 262).  Short contexts of few sequences take it further, while
+  // twice (64 x 8 k keys, 28 rows: 200 us against 239 in tcgen05 tiles; 35 rows:
+  // 290 against 240).  Short contexts of few sequences take it further, while
   // clusters of all their tiles are resident together (901 keys, 144 rows: 12
   // us against 14.5, and one launch).
   p->rows = per * G <= 8 ? 8 : per * G > 32 && (tiles_of(16) * 8 > 3 * sms || max_kv > 1024) ? 256 : 16;
   const int64_t tiles = tiles_of(p->rows);
   const int64_t slots = static_cast<int64_t>(sms) * 3;  // resident CTAs of the rows kernel
   p->stream = p->cluster = 0;
+  p->alternate = p->rows == 256 && per * G <= 128;
   int64_t want;
   if (p->rows <= 16) {
     // Ranges for about 7/4 CTAs a slot, at most a cluster's 8.  The even

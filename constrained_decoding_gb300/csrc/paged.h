@@ -62,9 +62,10 @@ int launch_kv_append(const AppendArgs& a, int sms, cudaStream_t s);
 // 256: tcgen05).  n_splits: ranges that every item's keys are divided into, walked
 // by a thread-block cluster that joins them (cluster) or joined by a second
 // kernel; with stream, CTAs that share the blocks of all items evenly.  parts:
-// of a row for that kernel, as far as the host knows.
+// of a row for that kernel, as far as the host knows.  alternate: items of one
+// tcgen05 tile give their key blocks to two pipelines in turn.
 struct PagedPlan {
-  int rows, n_splits, cluster, stream, parts;
+  int rows, n_splits, cluster, stream, parts, alternate;
 };
 
 struct PagedAttnArgs {

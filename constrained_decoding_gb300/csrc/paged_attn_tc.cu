@@ -20,6 +20,16 @@
 // have columns of their own, so S of the next block is made as soon as the
 // softmax holds the present scores, and its threads never wait for the MMAs.
 //
+// An item of one tile only (33 to 128 rows) gives its even and odd key blocks to
+// the two pipelines instead, with the second Q tile's place for codes of odd
+// blocks, and joins their states at the end.  64 sequences of 56 rows over 8 k
+// keys: 241 us against 274 (one pipeline).  Kernels for more rows are compiled
+// without it: its registers cost them 2%.
+//
+// Measured: 2 x 2048 tokens of 28 heads at the end of 8 k keys 371 us, 1135
+// TFLOP/s, bound by the chain of a tile's block (softmax 1900 clocks, P V 550, S
+// 600, four hand-offs of about 200); 9 prompts of heads of 64, 58 us.
+//
 // Registers: 512 threads launch with 128 each; the two softmax warpgroups
 // hold a row of 128 scores and take 192, paid for by the other two (64 each):
 // 64 + 64 + 192 + 192 = 4 x 128.
@@ -51,9 +61,9 @@ struct TileCfg {
   static constexpr int kOffV = kOffK + 2 * kOp;
   static constexpr int kRaw = kBlock * D;               // a block's K or V codes
   static constexpr int kOffRaw = kOffV + 2 * kOp;       // K's, then V's
-  static constexpr int kOffSc = kOffRaw + 2 * kRaw;     // [4][8] float4: constants of 16 keys
-  static constexpr int kOffWhole = kOffSc + 4 * 8 * 16;  // [4]: is every key of the block there?
-  static constexpr int kOffBar = kOffWhole + 16;
+  static constexpr int kOffSc = kOffRaw + 2 * kRaw;     // [8][8] float4: constants of 16 keys
+  static constexpr int kOffWhole = kOffSc + 8 * 8 * 16;  // [8]: is every key of the block there?
+  static constexpr int kOffBar = kOffWhole + 32;
   static constexpr int kSmem = kOffBar + 256 + 1024;    // + alignment slack
   static constexpr bool kOwnP = D == 64;                // the weights' columns: their own, or S's
   static constexpr int kColO = 2 * kBlock, kColP = kOwnP ? kColO + 2 * D : 0, kStepP = kOwnP ? kBlock / 2 : kBlock;
@@ -118,7 +128,7 @@ __device__ __forceinline__ uint32_t swz128(int row, int chunk) {  // 16-byte chu
   return static_cast<uint32_t>(row * 128 + ((chunk ^ (row & 7)) << 4));
 }
 
-template <int D, int FMT, class T>
+template <int D, int FMT, class T, bool ALT>
 __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a) {
   using C = TileCfg<D>;
   extern __shared__ uint8_t tile_raw[];
@@ -132,12 +142,12 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
   uint64_t* p_full = bars + 10;  // [tile] weights in TMEM
   uint64_t* pv_done = bars + 12; // [tile] O current, S columns free
   uint64_t* q_full = bars + 14;  // [tile] Q rows staged
-  uint64_t* raw_full = bars + 16;  // [K, V] codes landed, constants written
-  uint64_t* raw_free = bars + 18;  // [K, V] codes converted
-  uint64_t* turn = bars + 20;    // [tile] its issuer's turn
-  uint64_t* drain = bars + 22;   // [tile] its issuer's MMAs are done
-  uint64_t* s_free = bars + 24;  // [tile] scores are in the softmax's registers (weights with columns of their own)
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 26);
+  uint64_t* turn = bars + 16;    // [tile] its issuer's turn
+  uint64_t* drain = bars + 18;   // [tile] its issuer's MMAs are done
+  uint64_t* s_free = bars + 20;  // [tile] scores are in the softmax's registers (weights with columns of their own)
+  uint64_t* raw_full = bars + 22;  // [K, V; K, V of odd blocks] codes landed, constants written
+  uint64_t* raw_free = bars + 26;  // ... codes converted
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + 30);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   float4* sc = reinterpret_cast<float4*>(smem + C::kOffSc);
   volatile int* whole_block = reinterpret_cast<volatile int*>(smem + C::kOffWhole);
@@ -170,6 +180,13 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
   const int per = (bl + a.plan.n_splits - 1) / a.plan.n_splits;  // this item's blocks, in even ranges
   const int b0 = min(bl, z * per);
   const int nb = min(bl, b0 + per) - b0;
+  // One tile of rows: both pipelines take it, the even blocks and the odd ones.
+  // Block i is then pipeline i & 1's, stage i & 1 belongs to it alone, and the
+  // second Q tile's place holds the codes of odd blocks.
+  const bool alt = ALT && !two && nb > 1;
+  auto raw_at = [&](int i, int kv) { return smem + (alt && (i & 1) ? C::kOp : C::kOffRaw) + kv * C::kRaw; };
+  auto raw_bar = [&](int i, int kv) { return alt && (i & 1) ? kv + 2 : kv; };
+  auto raw_par = [&](int i) { return static_cast<uint32_t>((alt ? i >> 1 : i) & 1); };
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < 2; ++s) {
@@ -182,10 +199,12 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
       mbar_init(&pv_done[s], 1);
       mbar_init(&q_full[s], 4);
       mbar_init(&raw_full[s], 1);
+      mbar_init(&raw_full[s + 2], 1);
       mbar_init(&turn[s], 1);
       mbar_init(&s_free[s], 4);
       mbar_init(&drain[s], 1);
       mbar_init(&raw_free[s], 4);
+      mbar_init(&raw_free[s + 2], 4);
     }
     *abort_flag = 0;
     fence_mbar_init();
@@ -209,7 +228,7 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
 
   if (warp < 4) {
     regs_down<64>();
-    if ((warp == 0 || (warp == 2 && two)) && nb > 0) {
+    if ((warp == 0 || (warp == 2 && (two || alt))) && nb > 0) {
       // ------------------------------------------------------------ MMA issuers, one a tile
       // A warp stays together and one lane issues, so that descriptors are
       // computed in uniform registers (a lone lane took 20 more clocks an MMA).
@@ -218,7 +237,7 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
       const int t = __shfl_sync(0xffffffffu, warp >> 1, 0);
       const uint32_t tb = __shfl_sync(0xffffffffu, tbase, 0);
       const uint32_t dS = tb + t * kBlock, dO = tb + C::kColO + t * D;
-      const uint64_t dq = sdesc_kmajor_sw128(smem_u32(smem + t * C::kOp)), dk = sdesc_kmajor_sw128(smem_u32(smem + C::kOffK));
+      const uint64_t dq = sdesc_kmajor_sw128(smem_u32(smem + (alt ? 0 : t * C::kOp))), dk = sdesc_kmajor_sw128(smem_u32(smem + C::kOffK));
       const uint64_t dv = sdesc_mnmajor_sw128(smem_u32(smem + C::kOffV), kHalf, 1024);
       auto issue_s = [&](int st) {
         tc_fence_after_sync();
@@ -237,19 +256,21 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
         __syncwarp();
       };
       // turn[t] completes once before each of the tile's turns; the first tile's first turn is free
-      bool ok = mbar_wait(&k_full[0], 0, kWaitNs) && mbar_wait(&q_full[t], 0, kWaitNs) &&
-                (t == 0 || C::kOwnP || mbar_wait(&turn[1], 0, kWaitNs));
+      const int step = alt ? 2 : 1, i0 = alt ? t : 0;
+      bool ok = mbar_wait(&k_full[i0], 0, kWaitNs) && mbar_wait(&q_full[alt ? 0 : t], 0, kWaitNs) &&
+                (t == 0 || alt || C::kOwnP || mbar_wait(&turn[1], 0, kWaitNs));
       ok = __all_sync(0xffffffffu, ok);
-      if (ok) issue_s(0);
+      if (ok) issue_s(i0);
       const uint32_t dP = C::kOwnP ? tb + C::kColP + t * C::kStepP : dS;
-      for (int i = 0; ok && i < nb; ++i) {
+      for (int i = i0; ok && i < nb; i += step) {
         const int st = i & 1;
-        const uint32_t par = static_cast<uint32_t>(i & 1);
+        const uint32_t par = static_cast<uint32_t>((alt ? i >> 1 : i) & 1);
         auto next_s = [&](uint64_t* freed) {
-          if (i + 1 >= nb) return;
-          ok = mbar_wait(&k_full[st ^ 1], static_cast<uint32_t>(((i + 1) >> 1) & 1), kWaitNs) && mbar_wait(freed, par, kWaitNs);
+          const int in = i + step;
+          if (in >= nb) return;
+          ok = mbar_wait(&k_full[in & 1], static_cast<uint32_t>((in >> 1) & 1), kWaitNs) && mbar_wait(freed, par, kWaitNs);
           ok = __all_sync(0xffffffffu, ok && !*abort_flag);
-          if (ok) issue_s(st ^ 1);
+          if (ok) issue_s(in & 1);
         };
         if (C::kOwnP) next_s(&s_free[t]);
         if (!ok) break;
@@ -260,7 +281,7 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
         if (!ok) break;
         tc_fence_after_sync();
         const uint64_t v = dv + st * (C::kOp >> 4);
-        const uint32_t acc = i > 0 ? 1u : 0u;
+        const uint32_t acc = i > i0 ? 1u : 0u;
         if (elect_one_sync()) {
 #pragma unroll
           for (int k = 0; k < kBlock / 16; ++k)
@@ -286,11 +307,27 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
         const int pg = (b << 7 >> a.c.page_log2) + lane;
         return lane < npg && pg <= last_page ? tab[pg] : -1;
       };
-      int id_next = fetch(b0);
+      // Ids are fetched two blocks ahead and scales one, so that no copy waits for them.
+      int id_next = fetch(b0), id_after = fetch(b0 + 1);
+      bool there_next;
+      float ks_next, vs_next;
+      auto fetch_scales = [&](int b, int id) {  // 16 keys of block b to a lane
+        const int cid = __shfl_sync(0xffffffffu, id >= 0 && id < a.c.n_pages ? id : -1, (lane * 16 >> a.c.page_log2) & 31);
+        there_next = lane < kBlock / 16 && cid >= 0 && b * kBlock + lane * 16 < len;
+        const int64_t at = static_cast<int64_t>(there_next ? cid : 0) * a.c.Hkv + hk;
+        ks_next = a.c.ks[at];
+        vs_next = a.c.vs[at];
+      };
+      fetch_scales(b0, id_next);
       bool ok = true;
       for (int i = 0; i < nb && ok; ++i) {
         const int id = id_next, j0 = (b0 + i) * kBlock;
-        if (i + 1 < nb) id_next = fetch(b0 + i + 1);
+        const bool there = there_next;
+        const float k_scale = ks_next;
+        float v_scale = vs_next;
+        id_next = id_after;
+        id_after = fetch(b0 + i + 2);
+        fetch_scales(b0 + i + 1, id_next);
         const bool good = id >= 0 && id < a.c.n_pages;
         if (lane < npg && j0 + lane * page < len && !good) record_error(a.err, DEV_BAD_INDEX);
         const int rows = good ? min(page, len - j0 - lane * page) : 0;
@@ -298,41 +335,39 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
         const int64_t off = (good ? id : 0) * a.c.page_stride + hk * a.c.head_stride;
 #pragma unroll 1
         for (int kv = 0; kv < 2 && ok; ++kv) {
-          if (i > 0) ok = mbar_wait(&raw_free[kv], static_cast<uint32_t>((i - 1) & 1), kWaitNs);
+          const int before = i - (alt ? 2 : 1);  // the block whose codes were here
+          if (before >= 0) ok = mbar_wait(&raw_free[raw_bar(before, kv)], raw_par(before), kWaitNs);
           ok = __all_sync(0xffffffffu, ok && !*abort_flag);
           if (!ok) break;
           const uint8_t* base = kv ? a.c.v : a.c.k;
-          uint8_t* raw = smem + C::kOffRaw + kv * C::kRaw;
+          uint8_t* raw = raw_at(i, kv);
+          uint64_t* full = &raw_full[raw_bar(i, kv)];
           if (kv == 0) {
-            // 16 keys to a lane: K scale, log2 and reciprocal of the V scale, seen or not
-            const int pl = lane * 16 >> a.c.page_log2;
-            const int cid = __shfl_sync(0xffffffffu, good ? id : -1, pl & 31);
-            const bool there = cid >= 0 && j0 + lane * 16 < len;
+            // K scale, log2 and reciprocal of the V scale, seen or not
             const uint32_t all = __ballot_sync(0xffffffffu, there) & 0xffu;
-            // block i - 4 has left the softmax: K of block i - 1 was converted, after V of block i - 2, for which
-            // the P V of block i - 4 were done
+            // block i - 8 has left the softmax: K of block i - 2 at least was converted, after V of blocks i - 3
+            // and i - 4, for which the P V of blocks i - 5 and i - 6 were done
             if (lane < kBlock / 16) {
               float4 c = make_float4(0.f, 0.f, 0.f, 0.f);
               if (there) {
-                float v = a.c.vs[static_cast<int64_t>(cid) * a.c.Hkv + hk];
-                if (v < kScaleFloor) v = kScaleFloor;  // a NaN stays
-                c = make_float4(a.c.ks[static_cast<int64_t>(cid) * a.c.Hkv + hk], lg2(v), 1.f / v, 1.f);
+                if (v_scale < kScaleFloor) v_scale = kScaleFloor;  // a NaN stays
+                c = make_float4(k_scale, lg2(v_scale), 1.f / v_scale, 1.f);
               }
-              sc[(i & 3) * 8 + lane] = c;
-              if (lane == 0) whole_block[i & 3] = all == 0xffu && len - j0 >= kBlock;
+              sc[(i & 7) * 8 + lane] = c;
+              if (lane == 0) whole_block[i & 7] = all == 0xffu && len - j0 >= kBlock;
             }
             __syncwarp();
           }
-          if (lane == 0) mbar_arrive_expect_tx(&raw_full[kv], total);
+          if (lane == 0) mbar_arrive_expect_tx(full, total);
           __syncwarp();
           if (rows_together) {
-            if (rows > 0) bulk_g2s(raw + lane * page * D, base + off, rows * D, &raw_full[kv]);
+            if (rows > 0) bulk_g2s(raw + lane * page * D, base + off, rows * D, full);
           } else {
             for (int p = 0; p < npg; ++p) {
               const int n = __shfl_sync(0xffffffffu, rows, p);
               const int64_t o = __shfl_sync(0xffffffffu, off, p);
               for (int r = lane; r < n; r += 32)
-                bulk_g2s(raw + (p * page + r) * D, base + o + r * a.c.tok_stride, D, &raw_full[kv]);
+                bulk_g2s(raw + (p * page + r) * D, base + o + r * a.c.tok_stride, D, full);
             }
           }
           raw_issued = 2 * i + kv + 1;
@@ -352,7 +387,7 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
     constexpr int kStep = kBlock / kPer;         // rows between them
     const int row0 = D == 128 ? (((tid >> 5) * 2 + (ph >> 1)) * 2 + ((q8 >> 2) ^ (ph & 1))) : ((tid >> 3) * 2 + (q8 >> 2));
     const int ch = D == 128 ? q8 : (q8 & 3);
-    const uint8_t* raw0 = smem + C::kOffRaw + row0 * D + ch * 16;
+    const int raw0 = row0 * D + ch * 16;
     const uint32_t dst0 = (ch >> 2) * kHalf + swz128(row0, (ch & 3) * 2), dst1 = (ch >> 2) * kHalf + swz128(row0, (ch & 3) * 2 + 1);
     bool ok = true;
     for (int i = 0; i < nb && ok; ++i) {
@@ -360,19 +395,19 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
       const int live = min(kBlock, len - (b0 + i) * kBlock);  // rows behind the last token read as zeros
 #pragma unroll 1
       for (int kv = 0; kv < 2; ++kv) {
-        ok = mbar_wait(&raw_full[kv], static_cast<uint32_t>(i & 1), kWaitNs);
+        ok = mbar_wait(&raw_full[raw_bar(i, kv)], raw_par(i), kWaitNs);
         if (ok && i >= 2) ok = mbar_wait(kv ? &v_free[st] : &k_free[st], static_cast<uint32_t>(((i - 2) >> 1) & 1), kWaitNs);
         ok = __all_sync(0xffffffffu, ok && !*abort_flag);
         if (!ok) break;
-        const bool whole = whole_block[i & 3] != 0;
-        const uint8_t* src = raw0 + kv * C::kRaw;
+        const bool whole = whole_block[i & 7] != 0;
+        const uint8_t* src = raw_at(i, kv) + raw0;
         uint8_t* dst = smem + (kv ? C::kOffV : C::kOffK) + st * C::kOp;
 #pragma unroll
         for (int j = 0; j < kPer; ++j) {
           uint4 v = *reinterpret_cast<const uint4*>(src + j * kStep * D);
           if (!whole) {
             const int row = row0 + j * kStep;
-            if (row >= live || sc[(i & 3) * 8 + (row >> 4)].w == 0.f) v = make_uint4(0u, 0u, 0u, 0u);
+            if (row >= live || sc[(i & 7) * 8 + (row >> 4)].w == 0.f) v = make_uint4(0u, 0u, 0u, 0u);
           }
           uint32_t h[8];
           codes4_half<FMT>(v.x, &h[0], &h[1]);
@@ -387,7 +422,7 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
         __syncwarp();
         if (lane == 0) {
           mbar_arrive(kv ? &v_full[st] : &k_full[st]);
-          mbar_arrive(&raw_free[kv]);
+          mbar_arrive(&raw_free[raw_bar(i, kv)]);
         }
       }
     }
@@ -397,8 +432,8 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
     regs_up<192>();
     const int t = (warp - 8) >> 2;
     const int rt = 32 * (warp & 3) + lane;  // row of the tile = TMEM lane
-    const int r = r0 + t * kTile + rt;
-    const bool active = t == 0 || two;
+    const int r = r0 + (alt ? 0 : t * kTile) + rt;
+    const bool active = t == 0 || two || alt;
     const bool valid = r < r_end;
     const int rr = min(r, r_end - 1);
     const int tok = it.row0 + rr / a.G, hq = hk * a.G + rr % a.G;
@@ -450,6 +485,7 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
 #pragma unroll
           for (int x = 0; x < 4; ++x) w[x] = pack2(to_f(v[j][2 * x]) * down, to_f(v[j][2 * x + 1]) * down);
         }
+        if (alt && t == 1) continue;  // the first pipeline stages the tile
         const bool in = r0 + t * kTile + row < r_end;  // rows behind the last are zeros
         *reinterpret_cast<uint4*>(q + swz128(row, c & 7)) =
             in ? make_uint4(w[0], w[1], w[2], w[3]) : make_uint4(0u, 0u, 0u, 0u);
@@ -459,14 +495,15 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full[t]);
       const int wmin = __reduce_min_sync(0xffffffffu, vis);  // keys that every row of the warp sees
-      for (int i = 0; i < nb; ++i) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&s_full[t], static_cast<uint32_t>(i & 1), kWaitNs) && !*abort_flag);
+      int n = 0;  // blocks done
+      for (int i = alt ? t : 0; i < nb; i += alt ? 2 : 1, ++n) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&s_full[t], static_cast<uint32_t>(n & 1), kWaitNs) && !*abort_flag);
         if (!ok) break;
         tc_fence_after_sync();
         float s[kBlock];
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld_32cols_async(ts + 32 * c, s + 32 * c);
-        const float4* cs = sc + (i & 3) * 8;
+        const float4* cs = sc + (i & 7) * 8;
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld_wait32(s + 32 * c);
         if (C::kOwnP) {
@@ -475,7 +512,7 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
           if (lane == 0) mbar_arrive(&s_free[t]);
         }
         const int j0 = (b0 + i) * kBlock;
-        const bool plain = whole_block[i & 3] != 0 && j0 + kBlock <= wmin;
+        const bool plain = whole_block[i & 7] != 0 && j0 + kBlock <= wmin;
         float mx = -INFINITY;
 #pragma unroll
         for (int g = 0; g < 8; ++g) {
@@ -507,8 +544,8 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
         if (__any_sync(0xffffffffu, mx > m_ref + kSlackTc)) {
           const float m_new = fmaxf(m_ref, mx);
           const float f = m_ref == -INFINITY ? 0.f : ex2_approx(m_ref - m_new);
-          if (i > 0) {
-            ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[t], static_cast<uint32_t>((i - 1) & 1), kWaitNs));
+          if (n > 0) {
+            ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[t], static_cast<uint32_t>((n - 1) & 1), kWaitNs));
             if (!ok) break;
             tc_fence_after_sync();
 #pragma unroll 1
@@ -547,8 +584,8 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
             // a poisoned scale (NaN) counts only for rows that see its keys
             l = fmaf(sum.x + sum.y, plain || vis > j0 + 16 * g ? k.z : 0.f, l);
           }
-          if (C::kOwnP && q2 == 0 && i > 0) {  // the block before has left the weights' columns
-            ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[t], static_cast<uint32_t>((i - 1) & 1), kWaitNs));
+          if (C::kOwnP && q2 == 0 && n > 0) {  // the block before has left the weights' columns
+            ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[t], static_cast<uint32_t>((n - 1) & 1), kWaitNs));
             tc_fence_after_sync();
           }
           tmem_st_16cols_async(tp + 16 * q2, w);
@@ -559,16 +596,47 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[t]);
       }
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[t], static_cast<uint32_t>((nb - 1) & 1), kWaitNs) && !*abort_flag);
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[t], static_cast<uint32_t>((n - 1) & 1), kWaitNs) && !*abort_flag);
       if (!ok && lane == 0) fail(DEV_WAIT_TIMEOUT_EPILOGUE);
       tc_fence_after_sync();
     }
+    bool have = ok && nb > 0;
+    // ---- the odd blocks' state, handed over in their stage of K (channels below D / 2) and V and their codes' place
+    float f0 = 1.f, f1 = 0.f;
+    auto handed = [&](int d) {  // channel d of this row
+      return reinterpret_cast<float*>(smem + (d < D / 2 ? C::kOffK : C::kOffV) + C::kOp) + (d % (D / 2)) * kTile + rt;
+    };
+    if (alt) {
+      float2* hml = reinterpret_cast<float2*>(smem + C::kOp) + rt;
+      if (t == 1) {
+        if (have) {
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            float o[32];
+            tmem_ld_32cols_async(to + 32 * c, o);
+            tmem_ld_wait32(o);
+#pragma unroll
+            for (int x = 0; x < 32; ++x) handed(32 * c)[x * kTile] = o[x];
+          }
+        }
+        *hml = make_float2(m_ref, l);
+      }
+      named_barrier_sync(1 + (warp & 3), 64);  // the two warps of these rows
+      if (t == 0) {
+        have = have && !*abort_flag;
+        const float2 ml = *hml;
+        const float m = fmaxf(m_ref, ml.x);
+        f0 = m_ref == -INFINITY ? 0.f : ex2_approx(m_ref - m);
+        f1 = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - m);
+        m_ref = m;
+        l = fmaf(l, f0, ml.y * f1);
+      }
+    }
     // ---- out = O / l, or the state of this key range
-    const bool have = ok && nb > 0;
     const bool split = a.plan.n_splits > 1;
     const int64_t prow = (static_cast<int64_t>(z) * a.q.n_tok + tok) * a.Hq + hq;
     const float il = l == 0.f ? 0.f : 1.f / l;
-    if (active) {
+    if (active && !(alt && t == 1)) {
       // The warp turns its rows through its part of the Q tile (every S is done), 256 bytes of a row at a
       // time, so that 16 lanes write them side by side.
       uint8_t* turn = smem + t * C::kOp + (warp & 3) * (C::kOp / 4);
@@ -589,6 +657,11 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
           if (have) {
             tmem_ld_32cols_async(to + d, o);
             tmem_ld_wait32(o);
+            if (alt) {
+              const float* other = handed(d);
+#pragma unroll
+              for (int x = 0; x < 32; ++x) o[x] = fmaf(o[x], f0, other[x * kTile] * f1);
+            }
           }
           const bool some = have && l != 0.f;
           if (split) {
@@ -640,9 +713,8 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
   tc_fence_before_sync();
   __syncthreads();
   if (warp == 1) {  // nothing of this CTA's copies may still be landing when it exits
-    const int k = (raw_issued + 1) / 2, v = raw_issued / 2;
-    if (k > 0) mbar_wait(&raw_full[0], static_cast<uint32_t>((k - 1) & 1), kDrainWaitNs);
-    if (v > 0) mbar_wait(&raw_full[1], static_cast<uint32_t>((v - 1) & 1), kDrainWaitNs);
+    for (int x = max(0, raw_issued - (alt ? 4 : 2)); x < raw_issued; ++x)
+      mbar_wait(&raw_full[raw_bar(x >> 1, x & 1)], raw_par(x >> 1), kDrainWaitNs);
   }
   if (warp == 0) {
     __syncwarp();
@@ -651,10 +723,10 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
   }
 }
 
-template <int D, int FMT, class T>
+template <int D, int FMT, class T, bool ALT>
 int launch_tile(const PagedAttnArgs& a, cudaStream_t s) {
   using C = TileCfg<D>;
-  auto kern = paged_attn_tile_kernel<D, FMT, T>;
+  auto kern = paged_attn_tile_kernel<D, FMT, T, ALT>;
   static KernelSetup setup;
   const cudaError_t r = setup.run(kern, C::kSmem);
   if (r != cudaSuccess) return r;
@@ -664,7 +736,9 @@ int launch_tile(const PagedAttnArgs& a, cudaStream_t s) {
 }
 template <int D, int FMT>
 int launch_tile_t(const PagedAttnArgs& a, cudaStream_t s) {
-  return a.dtype == PCD_DTYPE_BF16 ? launch_tile<D, FMT, __nv_bfloat16>(a, s) : launch_tile<D, FMT, __half>(a, s);
+  if (a.plan.alternate)
+    return a.dtype == PCD_DTYPE_BF16 ? launch_tile<D, FMT, __nv_bfloat16, true>(a, s) : launch_tile<D, FMT, __half, true>(a, s);
+  return a.dtype == PCD_DTYPE_BF16 ? launch_tile<D, FMT, __nv_bfloat16, false>(a, s) : launch_tile<D, FMT, __half, false>(a, s);
 }
 
 }  // namespace

@@ -359,6 +359,41 @@ def test_attention_many_sequences(paged, n_seq, q_len):
     check_attend(got, lse, R.attention(*a, True, 64 ** -0.5))
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("fmt,dtype,page,dim,heads,kv_heads,q_lens,kv_lens", [
+    ("e4m3", "f16", 16, 128, 7, 1, [18, 1, 7], [1409, 129, 256]),    # 126, 7 and 49 rows; odd and even numbers of blocks
+    ("int8", "bf16", 64, 64, 12, 2, [21, 13, 0, 20], [1281, 1100, 50, 19]),
+    ("e4m3", "bf16", 128, 128, 8, 2, [32, 8, 31, 9], [4500, 128, 385, 0]),  # exactly a tile; one block; no keys
+    ("int8", "f16", 32, 64, 5, 1, [1, 60, 1, 1], [1153, 700, 257, 1]),  # 300 rows among short items
+])
+def test_attention_one_tile_of_rows(paged, fmt, dtype, page, dim, heads, kv_heads, q_lens, kv_lens, causal):
+    """33 to 128 rows a sequence and KV head: the key blocks of an item go to
+    two pipelines in turn, whose states are joined."""
+    a = attend_case(fmt, dtype, page, dim, heads, kv_heads, q_lens, kv_lens, 6)
+    want = R.attention(*a, causal, dim ** -0.5)
+    for hint in (max(kv_lens), 5000, 10 ** 6):  # several ranges of keys, and more ranges than blocks
+        got, lse = paged.pcd_k_paged_attention(*a, causal=causal, max_kv=hint, return_lse=True)
+        check_attend(got, lse, want)
+
+
+def test_attention_one_tile_of_rows_masks(paged):
+    """Rows that see no key of the odd blocks, or none at all, beside rows that
+    do; a poisoned scale in an odd block reaches only the rows that see it."""
+    q_len, L = 100, 190  # row i sees 91 + i keys: rows 0 .. 37 none of block 1
+    a = list(attend_case("e4m3", "f16", 16, 128, 1, 1, [q_len, 110], [L, 60], 2))
+    kw = dict(max_kv=5000, return_lse=True)
+    got, lse = paged.pcd_k_paged_attention(*a, **kw)
+    check_attend(got, lse, R.attention(*a, True, 128 ** -0.5))
+    assert torch.isinf(lse[q_len:q_len + 50]).all() and torch.all(got[q_len:q_len + 50] == 0)
+    for t in (3, 4):
+        keep = a[t]
+        a[t] = a[t].clone()
+        a[t][a[7][0, 8].long(), 0] = float("nan")  # keys 128 .. 143
+        bad, _ = paged.pcd_k_paged_attention(*a, **kw)
+        assert torch.equal(bad[:38], got[:38]) and torch.isnan(bad[38:q_len]).all() and torch.equal(bad[q_len:], got[q_len:])
+        a[t] = keep
+
+
 @pytest.mark.parametrize("q_len", [1, 40])
 def test_attention_scales_far_apart(paged, q_len):
     """Blocks whose value scales lie 2^40 apart, weights that fall by 2^-60,
