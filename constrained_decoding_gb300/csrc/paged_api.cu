@@ -91,9 +91,9 @@ int view_seqs(const int32_t* q_off, const int32_t* kv_len, const int32_t* table,
   return PCD_OK;
 }
 
-// May a kernel that reads x and writes y element by element in place of the
-// other run on these two views?
-bool rope_overlap_ok(const void* x, const void* y, int64_t es, int n, int h, int d, int64_t xt, int64_t xh, int64_t yt,
+// May a kernel that reads the rows of x and then writes the same rows of y run
+// on these two views?  They are the same view, or share no element.
+bool views_ok(const void* x, const void* y, int64_t es, int n, int h, int d, int64_t xt, int64_t xh, int64_t yt,
                      int64_t yh) {
   if (x == y && (xt == yt || n <= 1) && (xh == yh || h <= 1)) return true;
   const int64_t xa = reinterpret_cast<int64_t>(x), ya = reinterpret_cast<int64_t>(y);
@@ -165,7 +165,7 @@ extern "C" int pcd_k_rope(const void* x, void* y, int dtype, int n_tok, int head
   PCD_REFUSE(x_tok < 0 || x_head < 0 || y_tok < 0 || y_head < 0, PCD_ERR_INVALID_ARG, "negative stride");
   PCD_REFUSE((heads > 1 && y_head < head_dim) || (n_tok > 1 && y_tok < head_dim), PCD_ERR_INVALID_ARG,
              "strides of y overlap rows");
-  PCD_REFUSE(!rope_overlap_ok(x, y, es, n_tok, heads, head_dim, x_tok, x_head, y_tok, y_head), PCD_ERR_INVALID_ARG,
+  PCD_REFUSE(!views_ok(x, y, es, n_tok, heads, head_dim, x_tok, x_head, y_tok, y_head), PCD_ERR_INVALID_ARG,
              "x and y overlap without being the same view");
   PCD_REFUSE(static_cast<int64_t>(n_tok) * head_dim >= (int64_t{1} << 31), PCD_ERR_INVALID_ARG,
              "n_tok * head_dim is under 2^31");
@@ -190,6 +190,8 @@ extern "C" int pcd_k_kv_append(const pcd_kv_pages* cache, const void* k, const v
   PCD_REFUSE(!k || !v || !aligned(k, es) || !aligned(v, es) || !aligned(pos, 4) || !aligned(dev_err, 4),
              PCD_ERR_INVALID_ARG, "NULL or unaligned pointer");
   PCD_REFUSE(k_tok < 0 || k_head < 0 || v_tok < 0 || v_head < 0, PCD_ERR_INVALID_ARG, "negative stride");
+  PCD_REFUSE(cache->k == cache->v || cache->k_scale == cache->v_scale, PCD_ERR_INVALID_ARG,
+             "cache: keys and values in one place");
   a.k = k;
   a.v = v;
   a.dtype = dtype;
@@ -240,6 +242,8 @@ extern "C" int pcd_k_paged_attention(const pcd_kv_pages* cache, const void* q, v
   PCD_REFUSE(q_tok < 0 || q_head < 0 || out_tok < 0 || out_head < 0, PCD_ERR_INVALID_ARG, "negative stride");
   PCD_REFUSE((n_q_heads > 1 && out_head < a.c.dim) || (n_tok > 1 && out_tok < a.c.dim), PCD_ERR_INVALID_ARG,
              "strides of out overlap rows");
+  PCD_REFUSE(!views_ok(q, out, 2, n_tok, n_q_heads, a.c.dim, q_tok, q_head, out_tok, out_head), PCD_ERR_INVALID_ARG,
+             "q and out overlap without being the same view");
   a.x = q;
   a.out = out;
   a.lse = lse;

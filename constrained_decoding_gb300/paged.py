@@ -197,7 +197,7 @@ def pcd_k_paged_attention(q, k_cache, v_cache, k_scale, v_scale, q_off, kv_len, 
     tokens of sequence s and see up to themselves (`causal`), or all kv_len[s]
     tokens.  Rows behind the last offset are not written.  max_kv: the longest
     kv_len, if the caller knows it (default: what the table holds); scale
-    defaults to head_dim ** -0.5.  Returns the output, and with return_lse the
+    defaults to head_dim ** -0.5.  `out` may be q.  Returns the output, and with return_lse the
     log-sum-exp [tokens, query heads] too.  `scratch` (uint8) replaces the
     workspace that is otherwise taken from torch's allocator."""
     c, dev, page, kv_heads, dim = _pages(k_cache, v_cache, k_scale, v_scale)

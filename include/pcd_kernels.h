@@ -188,7 +188,7 @@ int pcd_rope_freqs(int rot_dim, double theta, int scaling, double factor, double
  * else (i, i + rot_dim / 2).  transpose != 0 turns by -phi with the same amp:
  * the gradient of the rotation.  Token t is at pos[t], or base + t when pos is
  * NULL; any int32 position, negative ones included.  y may be x's own view;
- * another overlap is refused. */
+ * another overlap is refused, and so is n_tok * head_dim of 2^31 and more. */
 int pcd_k_rope(const void* x, void* y, int dtype, int n_tok, int heads, int head_dim, int64_t x_tok, int64_t x_head,
                int64_t y_tok, int64_t y_head, const int64_t* freqs, int rot_dim, int interleaved, float amp,
                const int32_t* pos, int base, int transpose, void* stream);
@@ -196,9 +196,9 @@ int pcd_k_rope(const void* x, void* y, int dtype, int n_tok, int heads, int head
 /* A pool of cache pages in 8 bits.  The K and V codes of (page, KV head, slot)
  * are head_dim bytes at page * page_stride + head * head_stride + slot *
  * token_stride of `k` and `v` (strides and bases multiples of 16 bytes,
- * token_stride at most 2^24), so both [page][head][slot] and [page][slot][head] orders serve.  A page holds
- * page_size (16, 32, 64 or 128) consecutive tokens of one sequence; each
- * (page, KV head) has one scale in k_scale / v_scale [n_pages][n_kv_heads],
+ * token_stride at most 2^24), so both [page][head][slot] and
+ * [page][slot][head] orders serve.  A page holds page_size (16, 32, 64 or
+ * 128) consecutive tokens of one sequence; each (page, KV head) has one scale in k_scale / v_scale [n_pages][n_kv_heads],
  * fp32: value = code * scale.  head_dim 64 or 128. */
 #define PCD_KV_E4M3 1 /* 8-bit floats, 4 exponent bits; scales are powers of two when written here, and no code is NaN */
 #define PCD_KV_INT8 2 /* signed integers, -127 .. 127 */
@@ -227,7 +227,8 @@ typedef struct {
  * two, exact while they stay normal; int8: rounded once more).  Codes round to
  * nearest even.  A NaN or infinity in a block's rows makes its scale so, and
  * all that is read from that block NaN.  A page that one call appends to
- * belongs to one sequence.  Nothing but the new tokens' pages is written. */
+ * belongs to one sequence.  Nothing but the new tokens' pages is written.
+ * Keys and values in one place are refused. */
 int pcd_k_kv_append(const pcd_kv_pages* cache, const void* k, const void* v, int dtype, int64_t k_tok, int64_t k_head,
                     int64_t v_tok, int64_t v_head, const int32_t* q_off, const int32_t* kv_len, const int32_t* table,
                     int n_seq, int n_tok, int table_stride, const int64_t* freqs, int rot_dim, int interleaved,
@@ -246,10 +247,12 @@ int pcd_k_kv_append(const pcd_kv_pages* cache, const void* k, const void* v, int
  * accumulated in fp32; codes enter the products exactly and a value's scale
  * joins the softmax weight before its rounding to fp16.  Keys of a page that
  * the table has out of range are not seen; a length beyond the table reads as
- * zero tokens.  max_kv: the longest kv_len, as far as the host knows it; it
- * sets how many key ranges run side by side, not what is computed.  `scratch`: 16-byte aligned, at least
- * pcd_k_paged_attention_scratch_bytes (the same sizes, the same GPU) bytes
- * that the call overwrites; calls that may overlap need their own. */
+ * zero tokens.  `out` may be q's own view; another overlap is refused.
+ * max_kv: the longest kv_len, as far as the host knows it; it sets how many
+ * key ranges run side by side, not what is computed.  `scratch`: 16-byte
+ * aligned, at least pcd_k_paged_attention_scratch_bytes (the same sizes, the
+ * same GPU) bytes that the call overwrites; calls that may overlap in time,
+ * captured graphs among them, need their own. */
 int64_t pcd_k_paged_attention_scratch_bytes(int n_tok, int n_seq, int n_q_heads, int n_kv_heads, int head_dim,
                                             int64_t max_kv);
 int pcd_k_paged_attention(const pcd_kv_pages* cache, const void* q, void* out, float* lse, int dtype, int n_q_heads,

@@ -506,6 +506,14 @@ def test_attention_unaligned_rows(paged, q_len):
         assert got is out and torch.equal(got, paged.pcd_k_paged_attention(q, *rest))
 
 
+@pytest.mark.parametrize("q_len,kv,hint", [(1, 901, None), (1, 9000, None), (3, 20000, None), (20, 4000, None), (300, 500, 1), (300, 500, 9000)])
+def test_attention_in_place(paged, q_len, kv, hint):
+    """The output over the queries, in every way a call is cut up."""
+    q, *rest = attend_case("int8", "f16", 64, 128, 14, 2, [q_len, q_len], [kv, kv // 2], 4)
+    want = paged.pcd_k_paged_attention(q, *rest, max_kv=hint)
+    assert paged.pcd_k_paged_attention(q, *rest, max_kv=hint, out=q) is q and torch.equal(q, want)
+
+
 def test_two_streams_at_once(paged):
     """Calls that overlap on two streams, each with its own workspace, and a
     page that two sequences share for reading."""

@@ -26,7 +26,7 @@ def rope(lib, **kw):
 
 def pages(**kw):
     from constrained_decoding_gb300 import _decls as D
-    a = dict(k=BASE, v=2 * BASE, k_scale=BASE, v_scale=BASE, page_stride=2 * 16 * 64, head_stride=16 * 64, token_stride=64,
+    a = dict(k=BASE, v=2 * BASE, k_scale=BASE, v_scale=3 * BASE, page_stride=2 * 16 * 64, head_stride=16 * 64, token_stride=64,
              n_pages=8, page_size=16, n_kv_heads=2, head_dim=64, format=1)
     a.update(kw)
     return D.pcd_kv_pages(**a)
@@ -122,6 +122,12 @@ def test_append_refuses(lib, kw):
     assert lib.pcd_last_error()
 
 
+@pytest.mark.parametrize("kw", [dict(v=BASE), dict(v_scale=BASE)])
+def test_append_refuses_keys_and_values_in_one_place(lib, kw):
+    assert append(lib, pages(**kw)) == INVALID
+    assert b"one place" in lib.pcd_last_error()
+
+
 @pytest.mark.parametrize("kw", [
     dict(dtype=1), dict(dtype=7), dict(hq=0), dict(hq=3), dict(hq=258), dict(scale=0.0), dict(scale=-1.0), dict(scale=float("nan")),
     dict(scale=float("inf")), dict(max_kv=-1), dict(n=2 ** 29, max_kv=0), dict(q=None), dict(out=None), dict(q=BASE + 1),
@@ -129,6 +135,7 @@ def test_append_refuses(lib, kw):
     dict(n_seq=-1), dict(ts=-1), dict(q_off=None), dict(kv_len=None), dict(table=None), dict(table=BASE + 2),
     dict(max_kv=100000, ts=10000, scratch=None), dict(max_kv=100000, ts=10000, scratch=BASE, sb=64),
     dict(max_kv=100000, ts=10000, scratch=BASE + 8, sb=1 << 40),
+    dict(out=BASE, ot=512), dict(out=BASE, oh=128, ot=512), dict(out=BASE + 128), dict(out=BASE - 256, qt=256, ot=512),
 ])
 def test_attention_refuses(lib, kw):
     assert attend(lib, **kw) == INVALID
