@@ -143,33 +143,6 @@ namespace {
 //   stay in the page) -> older codes rescaled if it grew -> new codes.
 // Bound by that chain: 14.4 k tokens of four fp16 heads of 128 take 15 to 17 us
 // (2.7 TB/s of rows read and codes written), one token each of 64 sequences 5 us.
-constexpr int kAppendThreads = 128;
-
-template <class T>
-__device__ __forceinline__ float append_value(const AppendArgs& a, bool is_v, const T* row, int d, int pos) {
-  if (is_v || d >= a.rope.rot) return to_f(row[d]);
-  const int half = a.rope.rot / 2;
-  int i, j, u;
-  bool second;
-  if (a.rope.interleaved) {
-    u = d >> 1;
-    i = d & ~1;
-    j = i + 1;
-    second = d & 1;
-  } else {
-    second = d >= half;
-    u = second ? d - half : d;
-    i = u;
-    j = u + half;
-  }
-  float c, s;
-  turn(pos, a.rope.freqs[u], &c, &s);
-  c *= a.rope.amp;
-  s *= a.rope.amp;
-  const float p = to_f(row[i]), q = to_f(row[j]);
-  return second ? q * c + p * s : p * c - q * s;
-}
-
 // The block of a CTA: its new rows and where they go.
 struct AppendBlock {
   int held, rows, row0, pos0;  // older tokens in the page; new rows, the first one's index and position
@@ -236,27 +209,56 @@ __device__ __forceinline__ float append_scale(const AppendArgs& a, const AppendB
   return scale;
 }
 
-// Any layout: a channel at a time, each value computed for the maximum and
-// again for its code.
+// Any layout: a thread takes two channels at a time, a pair or two neighbours
+// that do not turn, and the rotated rows wait in shared memory as fp32 for the
+// scale, so each pair's sine and cosine are computed once (14.4 k tokens of four
+// fp16 heads of 128, 54 channels turned: 24.6 us; a channel at a time, computed
+// for the maximum and again for its code, 113).
+constexpr int kAppendThreads = 256;
 template <class T>
 __global__ void __launch_bounds__(kAppendThreads) kv_append_any_kernel(AppendArgs a) {
   griddep_launch_dependents();
   griddep_wait();
+  extern __shared__ __align__(16) float append_rows[];
   const bool is_v = blockIdx.z != 0;
   AppendBlock b;
   if (!append_block(a, is_v, static_cast<int>(blockIdx.y), &b)) return;
-  const int D = a.c.dim, total = b.rows * D;
+  const int D = a.c.dim, ulog = D == 128 ? 6 : 5;  // pairs of a row: 2^ulog
   const T* src = static_cast<const T*>(is_v ? a.v : a.k) + (is_v ? a.v_head : a.k_head) * blockIdx.y;
   const int64_t ts = is_v ? a.v_tok : a.k_tok;
-  auto value = [&](int r, int d) {
-    return append_value(a, is_v, src + (b.row0 + r) * ts, d, a.pos ? a.pos[b.row0 + r] : b.pos0 + r);
-  };
+  const int half = a.rope.rot / 2;
+  const int u = threadIdx.x & ((1 << ulog) - 1);  // the thread's pair, in every row it takes
+  const bool turns = !is_v && u < half;
+  const int i = turns && !a.rope.interleaved ? u : 2 * u, j = turns && !a.rope.interleaved ? u + half : 2 * u + 1;
+  const int64_t freq = turns ? a.rope.freqs[u] : 0;
   uint32_t am = 0;
-  for (int e = threadIdx.x; e < total; e += kAppendThreads)
-    am = max(am, __float_as_uint(value(e / D, e % D)) & 0x7fffffffu);
-  const float inv = 1.f / append_scale(a, b, am);
-  for (int e = threadIdx.x; e < total; e += kAppendThreads)
-    b.dst[(b.held + e / D) * a.c.tok_stride + e % D] = encode(value(e / D, e % D) * inv, a.c.format);
+  for (int r = static_cast<int>(threadIdx.x) >> ulog; r < b.rows; r += kAppendThreads >> ulog) {
+    const T* row = src + (b.row0 + r) * ts;
+    float p = to_f(row[i]), q = to_f(row[j]);
+    if (turns) {
+      float c, s;
+      turn(a.pos ? a.pos[b.row0 + r] : b.pos0 + r, freq, &c, &s);
+      c *= a.rope.amp;
+      s *= a.rope.amp;
+      const float p0 = p;
+      p = p0 * c - q * s;
+      q = q * c + p0 * s;
+    }
+    append_rows[r * D + i] = p;
+    append_rows[r * D + j] = q;
+    am = max(am, max(__float_as_uint(p) & 0x7fffffffu, __float_as_uint(q) & 0x7fffffffu));
+  }
+  const float scale = append_scale(a, b, am);  // its barrier is also the rows'
+  const float inv = 1.f / scale;
+  for (int e = threadIdx.x; e < b.rows * (D / 4); e += kAppendThreads) {
+    const int r = e >> (ulog - 1), d = (e & (D / 4 - 1)) * 4;
+    const float4 x = *reinterpret_cast<const float4*>(&append_rows[r * D + d]);
+    const float v[4] = {x.x, x.y, x.z, x.w};
+    uint32_t y = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) y |= static_cast<uint32_t>(encode(v[k] * inv, a.c.format)) << (8 * k);
+    *reinterpret_cast<uint32_t*>(b.dst + (b.held + r) * a.c.tok_stride + d) = y;
+  }
 }
 
 // Rows of whole 16-byte chunks: a thread holds NU units of a row's 16 channels
@@ -381,8 +383,13 @@ int launch_append_t(const AppendArgs& a, int sms, cudaStream_t s) {
   uint64_t m = reinterpret_cast<uintptr_t>(a.k) | reinterpret_cast<uintptr_t>(a.v);
   m |= static_cast<uint64_t>(a.k_tok | a.k_head | a.v_tok | a.v_head) * sizeof(T);
   const bool chunks = m % 16 == 0 && a.rope.rot % (a.rope.interleaved ? 8 : 16) == 0;
-  if (!chunks)
-    return launch_k(kv_append_any_kernel<T>, dim3(items, static_cast<unsigned>(a.c.Hkv), 2), dim3(kAppendThreads), 0, s, a);
+  if (!chunks) {
+    const int smem = (a.c.dim << a.c.page_log2) * 4;  // a page's rows: 4 to 64 KB
+    static KernelSetup setup;
+    const cudaError_t r = setup.run(kv_append_any_kernel<T>, 128 * 128 * 4);
+    if (r != cudaSuccess) return r;
+    return launch_k(kv_append_any_kernel<T>, dim3(items, static_cast<unsigned>(a.c.Hkv), 2), dim3(kAppendThreads), smem, s, a);
+  }
   // several heads a CTA where the pages alone fill the GPU
   const int64_t pages = static_cast<int64_t>(a.q.n_tok) >> a.c.page_log2;
   return 2 * pages >= 2ll * sms ? launch_append_h<T, 4>(a, items, s) : launch_append_h<T, 1>(a, items, s);

@@ -200,6 +200,9 @@ def check_append(before, after, scale_before, scale_after, x, x_err, new, lens, 
     ("f32", 64, 64, 1, [64, 65], [0, 0], 18, True, "head"),
     ("f16", 16, 64, 6, [2500, 40], [7, 0], 48, False, "head"),     # several heads of a page to a CTA, the last group short
     ("bf16", 32, 64, 5, [5000], [0], 64, True, "slot"),
+    ("bf16", 128, 128, 2, [300, 129, 1, 2], [0, 127, 200, 254], 54, False, "slot"),  # pairs that end inside a chunk
+    ("f16", 64, 128, 3, [190, 64], [33, 64], 12, True, "head"),
+    ("f32", 32, 64, 2, [75], [5], 2, False, "head"),
 ])
 def test_append(paged, fmt, dtype, page, dim, heads, new, old, rot, inter, order):
     table, kc, vc, ks, vs, k, v, q_off, kv_len, n = append_case(fmt, dtype, page, dim, heads, new, old, rot, inter, order, seed=page + dim)
