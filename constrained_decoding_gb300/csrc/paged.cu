@@ -23,7 +23,7 @@ namespace {
 // layout) of every hgs-th head of one token, so an angle's sine and cosine are
 // computed once for all of them, and takes two heads' loads at a time (four cost
 // registers and 4 us of 25 at 8192 tokens x 32 heads).  That call, fp16 heads of
-// 128: 24.7 us, 5.4 TB/s; 64 tokens of 28 heads 2.1 us.
+// 128: 24.7 us, 5.4 TB/s; 64 tokens of 14 heads 2.1 us.
 // VEC: the widest access that pointers, strides and the pair layout allow.
 template <class T, int N>
 struct alignas(sizeof(T) * N) Chunk {

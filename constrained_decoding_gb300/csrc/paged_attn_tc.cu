@@ -26,9 +26,12 @@
 // keys: 241 us against 274 (one pipeline).  Kernels for more rows are compiled
 // without it: its registers cost them 2%.
 //
-// Measured: 2 x 2048 tokens of 28 heads at the end of 8 k keys 371 us, 1135
-// TFLOP/s, bound by the chain of a tile's block (softmax 1900 clocks, P V 550, S
-// 600, four hand-offs of about 200); 9 prompts of heads of 64, 58 us.
+// Measured: 2 x 2048 tokens of 28 heads at the end of 8 k keys 372 us, 1130
+// TFLOP/s (bf16 387), bound by the chain of a tile's block (softmax 1900 clocks, P V 550, S
+// 600, four hand-offs of about 200); 9 prompts of heads of 64, 57 us.  An item's
+// start and end take some 15 k clocks: 2.3 to find its work, 4 to the first
+// converted K block with Q staged beside it, 2 to the first scores, 5 for the
+// output, 2 to the next CTA's entry.
 //
 // Registers: 512 threads launch with 128 each; the two softmax warpgroups
 // hold a row of 128 scores and take 192, paid for by the other two (64 each):
@@ -448,47 +451,74 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
       constexpr int kLanes = D / 8, kAt = 32 / kLanes;  // rows of one load
       const int64_t mine = tok * a.x_tok + hq * a.x_head;
       const int c = lane % kLanes;
-      alignas(16) T v[32 / kAt][8];
+      // (bf16 as whole words from either branch: elements, which their maxima want, would be taken apart where the
+      // branches meet, so that each load waited for the one before: 18 k clocks of a tile's start, now 8 k.  fp16
+      // words pass through untouched; loaded the other way their key loop came out 3% slower.)
+      uint4 v[32 / kAt];
+      if constexpr (std::is_same<T, __half>::value) {
+        alignas(16) T h[32 / kAt][8];
 #pragma unroll
-      for (int j = 0; j < 32 / kAt; ++j) {
-        const int r32 = j * kAt + lane / kLanes;
-        const T* src = static_cast<const T*>(a.x) + __shfl_sync(0xffffffffu, mine, r32) + 8 * c;
-        if (((reinterpret_cast<uintptr_t>(a.x) | static_cast<uint64_t>(a.x_tok | a.x_head) * 2) & 15) == 0) {
-          *reinterpret_cast<uint4*>(v[j]) = *reinterpret_cast<const uint4*>(src);
-        } else {
+        for (int j = 0; j < 32 / kAt; ++j) {
+          const T* src = static_cast<const T*>(a.x) + __shfl_sync(0xffffffffu, mine, j * kAt + lane / kLanes) + 8 * c;
+          if (((reinterpret_cast<uintptr_t>(a.x) | static_cast<uint64_t>(a.x_tok | a.x_head) * 2) & 15) == 0) {
+            *reinterpret_cast<uint4*>(h[j]) = *reinterpret_cast<const uint4*>(src);
+          } else {
 #pragma unroll
-          for (int x = 0; x < 8; ++x) v[j][x] = src[x];
+            for (int x = 0; x < 8; ++x) h[j][x] = src[x];
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 32 / kAt; ++j) v[j] = *reinterpret_cast<const uint4*>(h[j]);
+      } else if (((reinterpret_cast<uintptr_t>(a.x) | static_cast<uint64_t>(a.x_tok | a.x_head) * 2) & 15) == 0) {
+#pragma unroll
+        for (int j = 0; j < 32 / kAt; ++j)
+          v[j] = *reinterpret_cast<const uint4*>(static_cast<const T*>(a.x) +
+                                                 __shfl_sync(0xffffffffu, mine, j * kAt + lane / kLanes) + 8 * c);
+      } else {
+#pragma unroll 1
+        for (int j = 0; j < 32 / kAt; ++j) {
+          const uint16_t* src = static_cast<const uint16_t*>(a.x) + __shfl_sync(0xffffffffu, mine, j * kAt + lane / kLanes) + 8 * c;
+          uint32_t w[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) w[x] = src[2 * x] | static_cast<uint32_t>(src[2 * x + 1]) << 16;
+#pragma unroll
+          for (int k = 0; k < 32 / kAt; ++k)
+            if (k == j) v[k] = make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
       uint8_t* q = smem + t * C::kOp + (c >> 3) * kHalf;
       qs = 1.f;
+      if (!std::is_same<T, __half>::value) {  // all rows' maxima side by side: one chain of shuffles, not one a row
+        uint32_t am[32 / kAt];
 #pragma unroll
-      for (int j = 0; j < 32 / kAt; ++j) {
-        const int r32 = j * kAt + lane / kLanes, row = 32 * (warp & 3) + r32;
-        uint32_t w[4];
-        if (std::is_same<T, __half>::value) {
+        for (int j = 0; j < 32 / kAt; ++j) {
+          const uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+          am[j] = 0;
 #pragma unroll
-          for (int x = 0; x < 4; ++x) w[x] = reinterpret_cast<const uint32_t*>(v[j])[x];
-        } else {
-          uint32_t am = 0;
-#pragma unroll
-          for (int x = 0; x < 8; ++x) am = max(am, __float_as_uint(to_f(v[j][x])) & 0x7fffffffu);
-#pragma unroll
-          for (int o = kLanes / 2; o > 0; o >>= 1) am = max(am, __shfl_xor_sync(0xffffffffu, am, o));
-          float down;
-          const float up = row_power<T>(am, &down);
-#pragma unroll
-          for (int o = 0; o < kAt; ++o) {
-            const float u = __shfl_sync(0xffffffffu, up, o * kLanes);
-            if (lane == j * kAt + o) qs = u;
-          }
-#pragma unroll
-          for (int x = 0; x < 4; ++x) w[x] = pack2(to_f(v[j][2 * x]) * down, to_f(v[j][2 * x + 1]) * down);
+          for (int x = 0; x < 4; ++x) am[j] = max(am[j], max(w[x] << 16 & 0x7fffffffu, w[x] & 0x7fff0000u));
         }
-        if (alt && t == 1) continue;  // the first pipeline stages the tile
-        const bool in = r0 + t * kTile + row < r_end;  // rows behind the last are zeros
-        *reinterpret_cast<uint4*>(q + swz128(row, c & 7)) =
-            in ? make_uint4(w[0], w[1], w[2], w[3]) : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+        for (int o = kLanes / 2; o > 0; o >>= 1)
+#pragma unroll
+          for (int j = 0; j < 32 / kAt; ++j) am[j] = max(am[j], __shfl_xor_sync(0xffffffffu, am[j], o));
+#pragma unroll
+        for (int j = 0; j < 32 / kAt; ++j) {
+          float down;
+          const float u = __shfl_sync(0xffffffffu, row_power<T>(am[j], &down), (lane % kAt) * kLanes);
+          if (lane / kAt == j) qs = u;
+          uint32_t* w = reinterpret_cast<uint32_t*>(&v[j]);
+#pragma unroll
+          for (int x = 0; x < 4; ++x)  // bf16 are the upper halves of fp32
+            w[x] = pack2(__uint_as_float(w[x] << 16) * down, __uint_as_float(w[x] & 0xffff0000u) * down);
+        }
+      }
+      if (!alt || t == 0) {  // the first pipeline stages a tile that both take
+#pragma unroll
+        for (int j = 0; j < 32 / kAt; ++j) {
+          const int row = 32 * (warp & 3) + j * kAt + lane / kLanes;
+          const bool in = r0 + t * kTile + row < r_end;  // rows behind the last are zeros
+          *reinterpret_cast<uint4*>(q + swz128(row, c & 7)) = in ? v[j] : make_uint4(0u, 0u, 0u, 0u);
+        }
       }
       qs *= a.scale_log2;
       fence_proxy_async_smem();
