@@ -1130,7 +1130,20 @@ void plan_paged_attention(int n_tok, int n_seq, int G, int Hkv, int64_t max_kv, 
     want = p->stream ? slots : std::min<int64_t>(std::min<int64_t>(want, 8), (max_kv + 63) / 64);
     p->cluster = !p->stream && want > 1;
   } else {
-    want = std::min<int64_t>(sms / tiles, (max_kv + 127) / 128);
+    // The number of ranges with the least time by this account, in us: waves of
+    // CTAs, each 8 to start and end and 1.9 a key block, then the join's launch and
+    // the parts written and read (1 KB each).  Against one wave where that fits and
+    // else no ranges: 26 prompts of 4 to 90 tokens behind 7 k keys, 24 heads, 225 us
+    // for 241; 22 of 186 tokens, heads of 64, 169 for 176.
+    const int64_t blocks = std::max<int64_t>(1, (max_kv + 127) / 128);
+    double best = 0.0;
+    want = 1;
+    for (int64_t n = 1; n <= std::min(blocks, std::max<int64_t>(8, sms / tiles)); ++n) {
+      const double waves = static_cast<double>((tiles * n + sms - 1) / sms);
+      const double t = waves * (8.0 + 1.9 * static_cast<double>((blocks + n - 1) / n)) +
+                       (n > 1 ? 4.0 + n * static_cast<double>(n_tok) * G * Hkv * 2e-4 : 0.0);
+      if (n == 1 || t < best) best = t, want = n;
+    }
   }
   p->n_splits = static_cast<int>(std::max<int64_t>(want, 1));
   // parts of a row, about: an item may lie on several stretches
