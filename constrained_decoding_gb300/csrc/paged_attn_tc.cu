@@ -28,7 +28,7 @@
 //
 // Measured: 2 x 2048 tokens of 28 heads at the end of 8 k keys 372 us, 1130
 // TFLOP/s (bf16 387), bound by the chain of a tile's block (softmax 1900 clocks, P V 550, S
-// 600, four hand-offs of about 200); 9 prompts of heads of 64, 57 us.  An item's
+// 600, four hand-offs of about 200); 9 prompts of heads of 64, 56 us.  An item's
 // start and end take some 15 k clocks: 2.3 to find its work, 4 to the first
 // converted K block with Q staged beside it, 2 to the first scores, 5 for the
 // output, 2 to the next CTA's entry.
