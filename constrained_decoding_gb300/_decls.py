@@ -87,10 +87,16 @@ SIGNATURES = [
     ("pcd_k_kv_append", c_int, [c_void_p, c_void_p, c_void_p, c_int, c_int64, c_int64, c_int64, c_int64,
                                 c_void_p, c_void_p, c_void_p, c_int, c_int, c_int, c_void_p, c_int, c_int, c_float,
                                 c_void_p, c_void_p, c_void_p]),
+    ("pcd_k_kv_append_cols", c_int, [c_void_p, c_void_p, c_void_p, c_int, c_int64, c_int64, c_int64, c_int64,
+                                     c_void_p, c_void_p, c_void_p, c_int, c_int, c_int, c_int, c_void_p, c_int, c_int,
+                                     c_float, c_void_p, c_void_p, c_void_p]),
     ("pcd_k_paged_attention_scratch_bytes", c_int64, [c_int, c_int, c_int, c_int, c_int, c_int64]),
     ("pcd_k_paged_attention", c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_int, c_int64, c_int64,
                                       c_int64, c_int64, c_void_p, c_void_p, c_void_p, c_int, c_int, c_int, c_int64,
                                       c_int, c_float, c_void_p, c_int64, c_void_p, c_void_p]),
+    ("pcd_k_paged_attention_cols", c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_int, c_int64, c_int64,
+                                           c_int64, c_int64, c_void_p, c_void_p, c_void_p, c_int, c_int, c_int, c_int,
+                                           c_int64, c_int, c_float, c_void_p, c_int64, c_void_p, c_void_p]),
 ]
 
 

@@ -157,7 +157,7 @@ __device__ __forceinline__ bool append_block(const AppendArgs& a, bool is_v, int
   const int n = it.n, len = it.len;
   if (n == 0) return false;
   if (n < 0 || it.row0 < 0 || n > a.q.n_tok - it.row0 || len < n || len > kMaxLen ||
-      len > static_cast<int64_t>(a.q.table_stride) << a.c.page_log2) {
+      len > static_cast<int64_t>(a.q.table_width) << a.c.page_log2) {
     if (threadIdx.x == 0) record_error(a.err, DEV_BAD_INDEX);
     return false;
   }
@@ -470,7 +470,7 @@ __device__ __forceinline__ RowsSeq rows_seq(const PagedAttnArgs& a, int row0, in
     return q;
   }
   q.tiles = (n * a.G + ROWS - 1) / ROWS;
-  if (len < 0 || len > kMaxLen || len > static_cast<int64_t>(a.q.table_stride) << a.c.page_log2) {
+  if (len < 0 || len > kMaxLen || len > static_cast<int64_t>(a.q.table_width) << a.c.page_log2) {
     record_error(a.err, DEV_BAD_INDEX);
     q.len = 0;
   }

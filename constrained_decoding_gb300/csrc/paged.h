@@ -40,10 +40,11 @@ struct PagesView {
 };
 
 // Ragged sequences: query (or new) rows q_off[s] .. q_off[s + 1), kv_len[s]
-// tokens in the cache with them included, pages table[s * table_stride ..].
+// tokens in the cache with them included, their pages the first entries of the
+// table_width at table[s * table_stride].
 struct SeqView {
   const int32_t *q_off, *kv_len, *table;
-  int n_seq, n_tok, table_stride;
+  int n_seq, n_tok, table_stride, table_width;
 };
 
 struct AppendArgs {

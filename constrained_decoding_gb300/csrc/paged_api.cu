@@ -80,14 +80,15 @@ int view_pages(const pcd_kv_pages* c, pcd::PagesView* v) {
 }
 
 int view_seqs(const int32_t* q_off, const int32_t* kv_len, const int32_t* table, int n_seq, int n_tok, int table_stride,
-              pcd::SeqView* v) {
-  PCD_REFUSE(n_seq < 0 || n_tok < 0 || table_stride < 0 || n_seq > kMaxSeqs || n_tok > kMaxRows, PCD_ERR_INVALID_ARG,
-             "sequences, rows or table width out of range");
-  PCD_REFUSE(n_seq > 0 && (!q_off || !kv_len || (table_stride > 0 && !table)), PCD_ERR_INVALID_ARG,
+              int table_width, pcd::SeqView* v) {
+  PCD_REFUSE(n_seq < 0 || n_tok < 0 || table_stride < 0 || table_width < 0 || n_seq > kMaxSeqs || n_tok > kMaxRows,
+             PCD_ERR_INVALID_ARG, "sequences, rows or table width out of range");
+  PCD_REFUSE(table_width > table_stride, PCD_ERR_INVALID_ARG, "table_width is at most table_stride");
+  PCD_REFUSE(n_seq > 0 && (!q_off || !kv_len || (table_width > 0 && !table)), PCD_ERR_INVALID_ARG,
              "q_off, kv_len or table: NULL");
   PCD_REFUSE(!aligned(q_off, 4) || !aligned(kv_len, 4) || !aligned(table, 4), PCD_ERR_INVALID_ARG,
              "q_off, kv_len or table: unaligned pointer");
-  *v = pcd::SeqView{q_off, kv_len, table, n_seq, n_tok, table_stride};
+  *v = pcd::SeqView{q_off, kv_len, table, n_seq, n_tok, table_stride, table_width};
   return PCD_OK;
 }
 
@@ -172,14 +173,14 @@ extern "C" int pcd_k_rope(const void* x, void* y, int dtype, int n_tok, int head
   return launched(pcd::launch_rope(a, device_sms(), static_cast<cudaStream_t>(stream)));
 }
 
-extern "C" int pcd_k_kv_append(const pcd_kv_pages* cache, const void* k, const void* v, int dtype, int64_t k_tok,
-                               int64_t k_head, int64_t v_tok, int64_t v_head, const int32_t* q_off,
-                               const int32_t* kv_len, const int32_t* table, int n_seq, int n_tok, int table_stride,
-                               const int64_t* freqs, int rot_dim, int interleaved, float amp, const int32_t* pos,
-                               int* dev_err, void* stream) {
+extern "C" int pcd_k_kv_append_cols(const pcd_kv_pages* cache, const void* k, const void* v, int dtype, int64_t k_tok,
+                                    int64_t k_head, int64_t v_tok, int64_t v_head, const int32_t* q_off,
+                                    const int32_t* kv_len, const int32_t* table, int n_seq, int n_tok, int table_stride,
+                                    int table_width, const int64_t* freqs, int rot_dim, int interleaved, float amp,
+                                    const int32_t* pos, int* dev_err, void* stream) {
   pcd::AppendArgs a{};
   int rc = view_pages(cache, &a.c);
-  if (rc == PCD_OK) rc = view_seqs(q_off, kv_len, table, n_seq, n_tok, table_stride, &a.q);
+  if (rc == PCD_OK) rc = view_seqs(q_off, kv_len, table, n_seq, n_tok, table_stride, table_width, &a.q);
   if (rc != PCD_OK) return rc;
   const int es = elem_size(dtype);
   PCD_REFUSE(!es, PCD_ERR_INVALID_ARG, "unknown dtype");
@@ -199,6 +200,15 @@ extern "C" int pcd_k_kv_append(const pcd_kv_pages* cache, const void* k, const v
   a.pos = pos;
   a.err = dev_err;
   return launched(pcd::launch_kv_append(a, device_sms(), static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" int pcd_k_kv_append(const pcd_kv_pages* cache, const void* k, const void* v, int dtype, int64_t k_tok,
+                               int64_t k_head, int64_t v_tok, int64_t v_head, const int32_t* q_off,
+                               const int32_t* kv_len, const int32_t* table, int n_seq, int n_tok, int table_stride,
+                               const int64_t* freqs, int rot_dim, int interleaved, float amp, const int32_t* pos,
+                               int* dev_err, void* stream) {
+  return pcd_k_kv_append_cols(cache, k, v, dtype, k_tok, k_head, v_tok, v_head, q_off, kv_len, table, n_seq, n_tok,
+                              table_stride, table_stride, freqs, rot_dim, interleaved, amp, pos, dev_err, stream);
 }
 
 namespace {
@@ -222,14 +232,15 @@ extern "C" int64_t pcd_k_paged_attention_scratch_bytes(int n_tok, int n_seq, int
   return attn_scratch(n_tok, n_q_heads, head_dim, p);
 }
 
-extern "C" int pcd_k_paged_attention(const pcd_kv_pages* cache, const void* q, void* out, float* lse, int dtype,
-                                     int n_q_heads, int64_t q_tok, int64_t q_head, int64_t out_tok, int64_t out_head,
-                                     const int32_t* q_off, const int32_t* kv_len, const int32_t* table, int n_seq,
-                                     int n_tok, int table_stride, int64_t max_kv, int causal, float scale, void* scratch,
-                                     int64_t scratch_bytes, int* dev_err, void* stream) {
+extern "C" int pcd_k_paged_attention_cols(const pcd_kv_pages* cache, const void* q, void* out, float* lse, int dtype,
+                                          int n_q_heads, int64_t q_tok, int64_t q_head, int64_t out_tok,
+                                          int64_t out_head, const int32_t* q_off, const int32_t* kv_len,
+                                          const int32_t* table, int n_seq, int n_tok, int table_stride, int table_width,
+                                          int64_t max_kv, int causal, float scale, void* scratch, int64_t scratch_bytes,
+                                          int* dev_err, void* stream) {
   pcd::PagedAttnArgs a{};
   int rc = view_pages(cache, &a.c);
-  if (rc == PCD_OK) rc = view_seqs(q_off, kv_len, table, n_seq, n_tok, table_stride, &a.q);
+  if (rc == PCD_OK) rc = view_seqs(q_off, kv_len, table, n_seq, n_tok, table_stride, table_width, &a.q);
   if (rc != PCD_OK) return rc;
   PCD_REFUSE(dtype != PCD_DTYPE_F16 && dtype != PCD_DTYPE_BF16, PCD_ERR_INVALID_ARG, "queries are fp16 or bf16");
   PCD_REFUSE(n_q_heads < 1 || n_q_heads % a.c.Hkv || n_q_heads / a.c.Hkv > 128, PCD_ERR_INVALID_ARG,
@@ -265,4 +276,14 @@ extern "C" int pcd_k_paged_attention(const pcd_kv_pages* cache, const void* q, v
     a.part_at = reinterpret_cast<int2*>(a.part_ml + parts);
   }
   return launched(pcd::launch_paged_attention(a, static_cast<cudaStream_t>(stream)));
+}
+
+extern "C" int pcd_k_paged_attention(const pcd_kv_pages* cache, const void* q, void* out, float* lse, int dtype,
+                                     int n_q_heads, int64_t q_tok, int64_t q_head, int64_t out_tok, int64_t out_head,
+                                     const int32_t* q_off, const int32_t* kv_len, const int32_t* table, int n_seq,
+                                     int n_tok, int table_stride, int64_t max_kv, int causal, float scale, void* scratch,
+                                     int64_t scratch_bytes, int* dev_err, void* stream) {
+  return pcd_k_paged_attention_cols(cache, q, out, lse, dtype, n_q_heads, q_tok, q_head, out_tok, out_head, q_off, kv_len,
+                                    table, n_seq, n_tok, table_stride, table_stride, max_kv, causal, scale, scratch,
+                                    scratch_bytes, dev_err, stream);
 }

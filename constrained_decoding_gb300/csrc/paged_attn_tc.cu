@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
   const int tiles = (R + kRowsCta - 1) / kRowsCta;
   if (it.local >= tiles) return;
   int len = it.len;
-  if (len < 0 || len > kMaxLen || len > static_cast<int64_t>(a.q.table_stride) << a.c.page_log2) {
+  if (len < 0 || len > kMaxLen || len > static_cast<int64_t>(a.q.table_width) << a.c.page_log2) {
     if (threadIdx.x == 0) record_error(a.err, DEV_BAD_INDEX);
     len = 0;
   }

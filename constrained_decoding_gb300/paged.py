@@ -159,6 +159,8 @@ def pcd_k_kv_append(k, v, k_cache, v_cache, k_scale, v_scale, q_off, kv_len, tab
     bfloat16) into the cache, the keys rotated on the way when `freqs` is given.
     Rows q_off[s] .. q_off[s + 1) become the last tokens of sequence s, which has
     kv_len[s] with them; token j of it lies in page table[s, j // page size].
+    (`table` may be a column slice of a wider one: a length beyond its own columns
+    is out of range.)
     `err` (int32, one element) is set nonzero when offsets, lengths or pages
     were out of range."""
     c, dev, _, kv_heads, dim = _pages(k_cache, v_cache, k_scale, v_scale)
@@ -168,11 +170,11 @@ def pcd_k_kv_append(k, v, k_cache, v_cache, k_scale, v_scale, q_off, kv_len, tab
         raise ValueError("k: float32, float16 or bfloat16 [tokens, KV heads, head dim]")
     n = shape[0]
     ks, vs = _rows(k, dev, shape, dtype, "k"), _rows(v, dev, shape, dtype, "v")
-    t, t_stride, _ = _table(table, n_seq, dev)
+    t, t_stride, width = _table(table, n_seq, dev)
     f, rot = _rope(freqs, dev, dim)
-    _launch(dev, "pcd_k_kv_append", _lib.pcd_k_kv_append, c, k.data_ptr(), v.data_ptr(), code, ks[0], ks[1],
+    _launch(dev, "pcd_k_kv_append", _lib.pcd_k_kv_append_cols, c, k.data_ptr(), v.data_ptr(), code, ks[0], ks[1],
             vs[0], vs[1], _ints(q_off, dev, n_seq + 1, "q_off"), _ints(kv_len, dev, n_seq, "kv_len"), t, n_seq, n, t_stride,
-            f, rot, interleaved, amp, _ints(pos, dev, n, "pos"), _ints(err, dev, 1, "err"))
+            width, f, rot, interleaved, amp, _ints(pos, dev, n, "pos"), _ints(err, dev, 1, "err"))
 
 
 def pcd_k_paged_attention_scratch_bytes(n_tok: int, n_seq: int, n_q_heads: int, n_kv_heads: int, head_dim: int,
@@ -223,9 +225,9 @@ def pcd_k_paged_attention(q, k_cache, v_cache, k_scale, v_scale, q_off, kv_len, 
         raise ValueError(f"scratch: contiguous bytes on cuda:{dev}")
     else:
         need = scratch.numel() * scratch.element_size()
-    _launch(dev, "pcd_k_paged_attention", _lib.pcd_k_paged_attention, c, q.data_ptr(), out.data_ptr(),
+    _launch(dev, "pcd_k_paged_attention", _lib.pcd_k_paged_attention_cols, c, q.data_ptr(), out.data_ptr(),
             lse.data_ptr() if return_lse else 0, _DTYPE[dtype], heads, qs[0], qs[1], os[0], os[1],
-            _ints(q_off, dev, n_seq + 1, "q_off"), _ints(kv_len, dev, n_seq, "kv_len"), t, n_seq, n, t_stride, max_kv, causal,
-            dim ** -0.5 if scale is None else scale, 0 if scratch is None else scratch.data_ptr(), need,
+            _ints(q_off, dev, n_seq + 1, "q_off"), _ints(kv_len, dev, n_seq, "kv_len"), t, n_seq, n, t_stride, width, max_kv,
+            causal, dim ** -0.5 if scale is None else scale, 0 if scratch is None else scratch.data_ptr(), need,
             _ints(err, dev, 1, "err"))
     return (out, lse) if return_lse else out

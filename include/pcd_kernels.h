@@ -214,7 +214,10 @@ typedef struct {
  * sequence may have none, and rows behind the last offset are left alone),
  * kv_len[s] counts the sequence's tokens in the cache with the new ones
  * included, and token j of it lies in page table[s * table_stride + j /
- * page_size], slot j % page_size.
+ * page_size], slot j % page_size.  A row of the table has table_stride entries;
+ * the forms ending in _cols take tables whose rows are the first table_width
+ * entries (at most table_stride) of wider ones, as a column slice has them: a
+ * length beyond those is out of range, and nothing behind them is read.
  *
  * Append: the n new tokens of sequence s become its tokens kv_len[s] - n ..
  * kv_len[s] - 1.  k, v [n_tok][n_kv_heads][head_dim] of `dtype` (strides in
@@ -233,6 +236,11 @@ int pcd_k_kv_append(const pcd_kv_pages* cache, const void* k, const void* v, int
                     int64_t v_tok, int64_t v_head, const int32_t* q_off, const int32_t* kv_len, const int32_t* table,
                     int n_seq, int n_tok, int table_stride, const int64_t* freqs, int rot_dim, int interleaved,
                     float amp, const int32_t* pos, int* dev_err, void* stream);
+int pcd_k_kv_append_cols(const pcd_kv_pages* cache, const void* k, const void* v, int dtype, int64_t k_tok,
+                         int64_t k_head, int64_t v_tok, int64_t v_head, const int32_t* q_off, const int32_t* kv_len,
+                         const int32_t* table, int n_seq, int n_tok, int table_stride, int table_width,
+                         const int64_t* freqs, int rot_dim, int interleaved, float amp, const int32_t* pos, int* dev_err,
+                         void* stream);
 
 /* Attention of q [n_tok][n_q_heads][head_dim] (dtype PCD_DTYPE_F16 or _BF16)
  * over the cache: out = softmax(scale q k^T) v per query head, query head h
@@ -260,6 +268,11 @@ int pcd_k_paged_attention(const pcd_kv_pages* cache, const void* q, void* out, f
                           const int32_t* kv_len, const int32_t* table, int n_seq, int n_tok, int table_stride,
                           int64_t max_kv, int causal, float scale, void* scratch, int64_t scratch_bytes, int* dev_err,
                           void* stream);
+int pcd_k_paged_attention_cols(const pcd_kv_pages* cache, const void* q, void* out, float* lse, int dtype, int n_q_heads,
+                               int64_t q_tok, int64_t q_head, int64_t out_tok, int64_t out_head, const int32_t* q_off,
+                               const int32_t* kv_len, const int32_t* table, int n_seq, int n_tok, int table_stride,
+                               int table_width, int64_t max_kv, int causal, float scale, void* scratch,
+                               int64_t scratch_bytes, int* dev_err, void* stream);
 
 #ifdef __cplusplus
 }

@@ -1,0 +1,77 @@
+"""Calls of rotary positions and the 8-bit paged cache as their documentation
+allows them and programs make them: block tables cut out of wider ones, bad
+offsets and lengths beside good ones, outputs in odd places."""
+import math
+
+import pytest
+import torch
+
+import paged_ref as R
+from paged_ref import i32, offsets
+from test_gpu_paged import append_case, attend_case, check_append, check_attend, gen, paged  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+# -------------------------------------------------------------- table slices
+def in_wider(table, left, fill):
+    """The same table as the last columns of one that is `left` entries wider: its last row ends with the storage."""
+    big = torch.full((table.shape[0], left + table.shape[1]), fill, dtype=torch.int32, device="cuda")
+    big[:, left:] = table
+    return big[:, left:]
+
+
+@pytest.mark.parametrize("q_len,hint", [(1, None), (3, 20000), (20, None), (60, 20000), (300, 1)])
+def test_attention_table_slice(paged, q_len, hint):  # noqa: F811
+    """A column slice gives what its own columns say: a length beyond them
+    reads as no tokens and is reported, also where the wider table goes on."""
+    lens = [310, 400, 330]
+    a = list(attend_case("e4m3", "f16", 16, 128, 7, 1, [q_len] * 3, lens, 3))
+    want = paged.pcd_k_paged_attention(*a, max_kv=hint)
+    table = a[7]
+    a[7] = in_wider(table, 9, 0)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = paged.pcd_k_paged_attention(*a, max_kv=hint, err=err)
+    assert int(err) == 0 and torch.equal(got, want)
+    width = table.shape[1] * 16
+    for s in (1, 2):
+        for wrong in (width + 1, width + 9 * 16):
+            bad = list(lens)
+            bad[s] = wrong
+            a[6] = i32(bad)
+            err.zero_()
+            got, l = paged.pcd_k_paged_attention(*a, max_kv=hint, return_lse=True, err=err)
+            assert int(err) == 5
+            a[6] = i32([0 if i == s else n for i, n in enumerate(lens)])
+            check_attend(got, l, R.attention(*a, True, 128 ** -0.5))
+            a[6] = i32(lens)
+
+
+@pytest.mark.parametrize("rot", [0, 64, 54])
+def test_append_table_slice(paged, rot):  # noqa: F811
+    """New rows go to the pages of the slice; a length beyond it writes nothing
+    and is reported, whatever pages stand in the columns behind."""
+    new, old = [4, 20, 5], [40, 60, 59]
+    table, kc, vc, ks, vs, k, v, q_off, kv_len, n = append_case("int8", "f16", 16, 64, 2, new, old, rot, False)
+    freqs = paged.pcd_rope_freqs(rot, 1e6)[0].cuda() if rot else None
+    start = [t.clone() for t in (kc, vc, ks, vs)]
+    want = [t.clone() for t in start]
+    paged.pcd_k_kv_append(k, v, *want, q_off, kv_len, table, freqs=freqs)
+    sliced = in_wider(table, 3, 0)  # page 0 stands behind every row's end but the last
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = [t.clone() for t in start]
+    paged.pcd_k_kv_append(k, v, *got, q_off, kv_len, sliced, freqs=freqs, err=err)
+    assert int(err) == 0 and all(torch.equal(a, b) for a, b in zip(got, want))
+    for s in (0, 2):
+        lens = kv_len.clone()
+        lens[s] = table.shape[1] * 16 + 2
+        err.zero_()
+        got = [t.clone() for t in start]
+        paged.pcd_k_kv_append(k, v, *got, q_off, lens, sliced, freqs=freqs, err=err)
+        assert int(err) == 5
+        first = (old[s]) // 16
+        mine = table[s, first:-(-(old[s] + new[s]) // 16)].long()
+        expect = [t.clone() for t in want]
+        for t, b in zip(expect, start):
+            t[mine] = b[mine]  # nothing of this sequence was written, all of the others'
+        assert all(torch.equal(a, b) for a, b in zip(got, expect))
