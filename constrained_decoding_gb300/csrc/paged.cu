@@ -152,7 +152,9 @@ struct AppendBlock {
 __device__ __forceinline__ bool append_block(const AppendArgs& a, bool is_v, int h, AppendBlock* b) {
   const int page = 1 << a.c.page_log2;
   // item -> (sequence, page of its new range)
+  const OffsetCheck offsets(a.q);
   const SeqItem it = find_item(a.q, static_cast<int>(blockIdx.x), 1, a.c.page_log2, 2);
+  offsets.report(a.q, a.err);
   if (it.seq < 0) return false;
   const int n = it.n, len = it.len;
   if (n == 0) return false;
@@ -532,7 +534,9 @@ __global__ void __launch_bounds__(kWarps * 32, 3) paged_attn_rows_kernel(PagedAt
     sq = rows_seq<ROWS>(a, seq);
   } else {
     // (what returns here returns in every CTA of a cluster)
+    const OffsetCheck offsets(a.q);
     const SeqItem it = find_item(a.q, static_cast<int>(blockIdx.x), a.G, ROWS == 8 ? 3 : 4, 1);
+    offsets.report(a.q, a.err);
     if (it.seq < 0) return;
     seq = it.seq;
     tile = it.local;

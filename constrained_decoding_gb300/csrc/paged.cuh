@@ -98,6 +98,22 @@ __device__ __forceinline__ SeqItem find_item(const SeqView& q, int idx, int mul,
     hi = min(hi, lo + step);
   }
 }
+// The offsets of sequence blockIdx.x, checked by one thread of the grid (every
+// grid of items has a CTA for each sequence): where offsets decrease, find_item
+// may lead no CTA to the sequence that has them.  Constructed before find_item,
+// so that the loads go out together.
+struct OffsetCheck {
+  int lo = 0, hi = 0;
+  __device__ __forceinline__ explicit OffsetCheck(const SeqView& q) {
+    if (threadIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0 && blockIdx.x < static_cast<unsigned>(q.n_seq)) {
+      lo = q.q_off[blockIdx.x];
+      hi = q.q_off[blockIdx.x + 1];
+    }
+  }
+  __device__ __forceinline__ void report(const SeqView& q, int* err) const {
+    if (lo != hi && (lo < 0 || hi < lo || hi > q.n_tok)) record_error(err, DEV_BAD_INDEX);
+  }
+};
 
 // ---------------------------------------------------------------------- codes
 constexpr float kScaleFloor = 8.673617379884035e-19f;  // 2^-60: a block of zeros has this scale

@@ -159,7 +159,9 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
   const int hk = blockIdx.y, z = blockIdx.z;
   griddep_launch_dependents();
   griddep_wait();
+  const OffsetCheck offsets(a.q);
   const SeqItem it = find_item(a.q, static_cast<int>(blockIdx.x), a.G, 8, 1);
+  offsets.report(a.q, a.err);
   if (it.seq < 0 || it.n == 0) return;
   if (it.n < 0 || it.row0 < 0 || it.n > a.q.n_tok - it.row0) {
     if (threadIdx.x == 0) record_error(a.err, DEV_BAD_INDEX);

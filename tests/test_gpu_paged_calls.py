@@ -75,3 +75,40 @@ def test_append_table_slice(paged, rot):  # noqa: F811
         for t, b in zip(expect, start):
             t[mine] = b[mine]  # nothing of this sequence was written, all of the others'
         assert all(torch.equal(a, b) for a, b in zip(got, expect))
+
+
+# ---------------------------------------------------------------- bad offsets
+# rows and hints that make every way a call is cut up: clusters, stretches, one and two tiles with ranges of keys and without
+CUTS = [(1, 400), (1, 20000), (3, 20000), (10, 20000), (10, 1), (60, 20000), (60, 1)]
+FAR = 2 ** 31 - 1
+
+
+def bad_offsets(q):
+    """Offsets of three sequences of q rows with something wrong in them, and the sequences whose rows they spoil."""
+    n = 3 * q
+    return [([0, q, 2 * q, FAR], [2]), ([0, q, 2 * q, n + 1], [2]), ([0, q, -7, n], [1, 2]), ([0, q, FAR, n], [1, 2]),
+            ([-3, q, 2 * q, n], [0]), ([0, 2 * q, q, n], [0, 1, 2]), ([0, 0, 2 * q, FAR], [0, 1, 2]), ([-9, -8, -8, n], [0, 1, 2])]
+
+
+@pytest.mark.parametrize("q_len,hint", CUTS)
+@pytest.mark.parametrize("empty", [0, 40])
+def test_bad_offsets_are_reported(paged, q_len, hint, empty):  # noqa: F811
+    """Every offset that is out of range or decreases is reported by the append
+    and by the attention, however the call is cut up; good ones are not, empty
+    sequences among them."""
+    lens = [310, 400, 330]
+    a = list(attend_case("e4m3", "f16", 16, 128, 7, 1, [q_len] * 3, lens, 3))
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    k = torch.randn(3 * q_len, 1, 128, generator=gen(1), device="cuda").half()
+    kv_len = i32(lens + [5] * empty)
+    table = torch.cat([a[7], a[7][:1].expand(empty, -1)]).contiguous()
+    good = [0, q_len, 2 * q_len, 3 * q_len]
+    for off in [good, [FAR] * 4] + [b for b, _ in bad_offsets(q_len)]:
+        q_off = i32(off + off[-1:] * empty)
+        want = 0 if len(set(off)) == 1 or off == good else 5
+        err.zero_()
+        paged.pcd_k_paged_attention(a[0], *a[1:5], q_off, kv_len, table, max_kv=hint, err=err)
+        assert int(err) == want, off
+        err.zero_()
+        paged.pcd_k_kv_append(k, k, *[t.clone() for t in a[1:5]], q_off, kv_len, table, err=err)
+        assert int(err) == want, off
