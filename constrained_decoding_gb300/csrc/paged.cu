@@ -973,6 +973,27 @@ __global__ void __launch_bounds__(kWarps * 32, 3) paged_attn_rows_kernel(PagedAt
   }
 }
 
+// Do the parts of row (tok, hq) come from this call?  Rows of no sequence and of
+// sequences with bad offsets have none: they stay as they are.
+__device__ __forceinline__ bool row_taken(const PagedAttnArgs& a, int tok, int hq) {
+  if (a.q.n_seq <= 32) {  // all offsets good, as nearly always: seen in one trip to memory
+    const int lane = threadIdx.x & 31;
+    int off = 0, end = 0;
+    if (lane < a.q.n_seq) {
+      off = a.q.q_off[lane];
+      end = a.q.q_off[lane + 1];
+    }
+    if (!__any_sync(0xffffffffu, off != end && (off < 0 || end < off || end > a.q.n_tok)))
+      return __any_sync(0xffffffffu, off <= tok && tok < end);
+  }
+  const SeqItem it = find_row(a.q, tok);
+  if (it.seq < 0 || a.plan.stream) return it.seq >= 0;
+  // where other offsets decrease, the tile kernel may not have found the row's item
+  const int tile = (it.local * a.G + hq % a.G) >> kTileRowsLog, tiles = (it.n * a.G + kTileRows - 1) >> kTileRowsLog;
+  const int item = (it.row0 * a.G >> kTileRowsLog) + it.seq + tiles - 1 - tile;
+  return find_item(a.q, item, a.G, kTileRowsLog, 1).seq == it.seq;
+}
+
 // Joins the parts of a row: out = sum 2^(M_i - M) O_i / sum 2^(M_i - M) l_i.
 // With ranges, part i is range i's state of the row; with stretches, the first
 // part is where part_at says and the others begin the stretches of the CTAs
@@ -989,11 +1010,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32) paged_attn_join_kernel(PagedA
   const int row = static_cast<int>(blockIdx.x) * (kJoinWarps / W) + warp / W;
   if (row >= a.q.n_tok * a.Hq) return;
   const int tok = row / a.Hq, hq = row % a.Hq;
-  if (tok < a.q.q_off[0] || tok >= a.q.q_off[a.q.n_seq]) return;  // rows of no sequence stay as they are
+  if (!row_taken(a, tok, hq)) return;
   int2 at = make_int2(0, a.plan.n_splits);
   if (a.plan.stream) {
     at = a.part_at[row];
-    // (rows between bad offsets were never described: what stands there is not followed out of range)
+    // (offsets that decrease may give a row to two sequences: nothing is followed out of range)
     const int cta = at.x >> 5;
     if (at.x < 0 || at.y < 1 || cta >= a.plan.n_splits || at.y > a.plan.n_splits - cta) return;
   }

@@ -64,11 +64,11 @@ struct SeqItem {
 // [f(s), f(s + 1)), f(s) = (q_off[s] * mul >> shift) + add * s: a bound on its
 // tiles that needs no prefix sum.  A warp narrows 32 ways at a time; lanes
 // fetch all that a sequence has at once, so up to 32 sequences cost one trip
-// to memory.
+// to memory.  (As unsigned, so that a negative offset stands behind every item.)
 __device__ __forceinline__ SeqItem find_item(const SeqView& q, int idx, int mul, int shift, int add) {
   const int lane = threadIdx.x & 31;
   auto f = [&](int off, int s) {
-    return static_cast<int>(static_cast<unsigned>(off) * static_cast<unsigned>(mul) >> shift) + add * s;
+    return (static_cast<unsigned>(off) * static_cast<unsigned>(mul) >> shift) + static_cast<unsigned>(add * s);
   };
   int lo = 0, hi = q.n_seq;
   while (true) {
@@ -82,7 +82,7 @@ __device__ __forceinline__ SeqItem find_item(const SeqView& q, int idx, int mul,
         len = q.kv_len[s];
       }
     }
-    const unsigned b = __ballot_sync(0xffffffffu, s < hi && f(off, s) <= idx);
+    const unsigned b = __ballot_sync(0xffffffffu, s < hi && f(off, s) <= static_cast<unsigned>(idx));
     if (b == 0) return SeqItem{-1, 0, 0, 0, 0};
     const int l = 31 - __clz(b);
     if (step == 1) {
@@ -91,12 +91,19 @@ __device__ __forceinline__ SeqItem find_item(const SeqView& q, int idx, int mul,
       it.row0 = __shfl_sync(0xffffffffu, off, l);
       it.n = static_cast<int>(static_cast<unsigned>(__shfl_sync(0xffffffffu, end, l)) - static_cast<unsigned>(it.row0));
       it.len = __shfl_sync(0xffffffffu, len, l);
-      it.local = idx - f(it.row0, it.seq);
+      it.local = static_cast<int>(static_cast<unsigned>(idx) - f(it.row0, it.seq));
       return it;
     }
     lo += l * step;
     hi = min(hi, lo + step);
   }
+}
+// The sequence of row `tok`; none (seq -1) for rows of no sequence and of those
+// whose offsets are bad, which every kernel skips.
+__device__ __forceinline__ SeqItem find_row(const SeqView& q, int tok) {
+  SeqItem it = find_item(q, tok, 1, 0, 0);
+  if (it.seq >= 0 && (it.row0 < 0 || it.n <= it.local || it.n > q.n_tok - it.row0)) it.seq = -1;
+  return it;
 }
 // The offsets of sequence blockIdx.x, checked by one thread of the grid (every
 // grid of items has a CTA for each sequence): where offsets decrease, find_item

@@ -65,6 +65,7 @@ int launch_kv_append(const AppendArgs& a, int sms, cudaStream_t s);
 // kernel; with stream, CTAs that share the blocks of all items evenly.  parts:
 // of a row for that kernel, as far as the host knows.  alternate: items of one
 // tcgen05 tile give their key blocks to two pipelines in turn.
+constexpr int kTileRowsLog = 8, kTileRows = 1 << kTileRowsLog;  // query rows of an item of the tcgen05 kernel
 struct PagedPlan {
   int rows, n_splits, cluster, stream, parts, alternate;
 };

@@ -51,6 +51,7 @@ namespace {
 
 constexpr int kTile = 128;        // rows of a tile (MMA M)
 constexpr int kRowsCta = 2 * kTile;
+static_assert(kRowsCta == kTileRows, "rows of an item");
 constexpr int kBlock = 128;       // keys of a block (MMA N of S, K of P V)
 constexpr int kHalf = kTile * 128;  // bytes of 64 channels x 128 rows, one 128-byte swizzled row each
 constexpr float kSlackTc = 7.f;
@@ -160,7 +161,7 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
   griddep_launch_dependents();
   griddep_wait();
   const OffsetCheck offsets(a.q);
-  const SeqItem it = find_item(a.q, static_cast<int>(blockIdx.x), a.G, 8, 1);
+  const SeqItem it = find_item(a.q, static_cast<int>(blockIdx.x), a.G, kTileRowsLog, 1);
   offsets.report(a.q, a.err);
   if (it.seq < 0 || it.n == 0) return;
   if (it.n < 0 || it.row0 < 0 || it.n > a.q.n_tok - it.row0) {

@@ -218,6 +218,9 @@ typedef struct {
  * the forms ending in _cols take tables whose rows are the first table_width
  * entries (at most table_stride) of wider ones, as a column slice has them: a
  * length beyond those is out of range, and nothing behind them is read.
+ * Offsets that decrease or leave the rows are reported, and the rows of their
+ * sequences are left alone; work finds its sequence by a search, so rows of other
+ * sequences of such a call may be left alone too.
  *
  * Append: the n new tokens of sequence s become its tokens kv_len[s] - n ..
  * kv_len[s] - 1.  k, v [n_tok][n_kv_heads][head_dim] of `dtype` (strides in

@@ -84,10 +84,11 @@ FAR = 2 ** 31 - 1
 
 
 def bad_offsets(q):
-    """Offsets of three sequences of q rows with something wrong in them, and the sequences whose rows they spoil."""
+    """Offsets of three sequences of q rows with something wrong in them, and what becomes of each third of the rows:
+    its sequence's output (g), left alone (-), or another sequence's (?)."""
     n = 3 * q
-    return [([0, q, 2 * q, FAR], [2]), ([0, q, 2 * q, n + 1], [2]), ([0, q, -7, n], [1, 2]), ([0, q, FAR, n], [1, 2]),
-            ([-3, q, 2 * q, n], [0]), ([0, 2 * q, q, n], [0, 1, 2]), ([0, 0, 2 * q, FAR], [0, 1, 2]), ([-9, -8, -8, n], [0, 1, 2])]
+    return [([0, q, 2 * q, FAR], "gg-"), ([0, q, 2 * q, n + 1], "gg-"), ([0, q, -7, n], "g--"), ([0, q, FAR, n], "g--"),
+            ([-3, q, 2 * q, n], "-gg"), ([-9, -8, -8, n], "---"), ([0, 0, 2 * q, FAR], "??-"), ([0, 2 * q, q, n], "???")]
 
 
 @pytest.mark.parametrize("q_len,hint", CUTS)
@@ -112,3 +113,61 @@ def test_bad_offsets_are_reported(paged, q_len, hint, empty):  # noqa: F811
         err.zero_()
         paged.pcd_k_kv_append(k, k, *[t.clone() for t in a[1:5]], q_off, kv_len, table, err=err)
         assert int(err) == want, off
+
+
+def attend_raw(paged, a, out, lse, max_kv, scratch, err, causal=True):  # noqa: F811
+    """The C call on the caller's own output, log-sum-exp and workspace."""
+    q, kc, vc, ks, vs, q_off, kv_len, table = a
+    c, _, _, _, dim = paged._pages(kc, vc, ks, vs)
+    rc = paged._lib.pcd_k_paged_attention(
+        c, q.data_ptr(), out.data_ptr(), lse.data_ptr(), 3 if q.dtype == torch.float16 else 2, q.shape[1], *q.stride()[:2],
+        *out.stride()[:2], q_off.data_ptr(), kv_len.data_ptr(), table.data_ptr(), kv_len.numel(), q.shape[0], table.shape[1],
+        max_kv, causal, dim ** -0.5, scratch.data_ptr(), scratch.numel(), err.data_ptr(), torch.cuda.current_stream().cuda_stream)
+    assert rc == 0
+
+
+@pytest.mark.parametrize("q_len,hint", CUTS)
+@pytest.mark.parametrize("dim,empty", [(64, 0), (128, 0), (128, 40)])
+def test_attention_leaves_skipped_rows(paged, q_len, hint, dim, empty):  # noqa: F811
+    """Rows of sequences with bad offsets keep what stood in the output and the
+    log-sum-exp, although the workspace holds states of an earlier call."""
+    lens = [310, 400, 330]
+    n = 3 * q_len
+    a = list(attend_case("e4m3", "f16", 32, dim, 7, 1, [q_len] * 3 + [0] * empty, lens + [9] * empty, 3))
+    size = paged.pcd_k_paged_attention_scratch_bytes(n, 3 + empty, 7, 1, dim, hint)
+    scratch = torch.zeros(max(size, 16), dtype=torch.uint8, device="cuda")
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+
+    def run(args, poison=None):
+        out = torch.full_like(args[0], 7.0)
+        lse = torch.full((n, 7), 7.0, device="cuda")
+        if poison is not None:
+            scratch.view(torch.int32)[:] = poison
+        err.zero_()
+        attend_raw(paged, args, out, lse, hint, scratch, err)
+        return out, lse
+
+    ref = R.attention(*a, True, dim ** -0.5)
+    good = run(a)
+    check_attend(*good, ref)
+    assert int(err) == 0
+    for off, becomes in bad_offsets(q_len):
+        for poison in (None, 0x3f800000, 0x00010000):  # states left by the good call; ones; small counts
+            run(a)
+            out, lse = run(a[:5] + [i32(off + off[-1:] * empty)] + a[6:], poison)
+            assert int(err) == 5
+            for s, what in enumerate(becomes):
+                rows = slice(s * q_len, (s + 1) * q_len)
+                if what == "-":
+                    assert torch.all(out[rows] == 7) and torch.all(lse[rows] == 7), off
+                elif what == "g" and not (empty and torch.all(out[rows] == 7)):  # (of many, a search may miss its neighbours)
+                    check_attend(out[rows], lse[rows], [t[rows] for t in ref])
+    # offsets that decrease: what is written is a sequence's own
+    out, lse = run(a[:5] + [i32([0, 2 * q_len, q_len, n] + [n] * empty)] + a[6:], 0x3f800000)
+    assert int(err) == 5
+    first = R.attention(a[0][:2 * q_len], *a[1:5], i32([0, 2 * q_len]), a[6][:1], a[7][:1], True, dim ** -0.5)
+    last = R.attention(a[0][q_len:], *a[1:5], i32([0, 2 * q_len]), a[6][2:3], a[7][2:3], True, dim ** -0.5)
+    for rows, want, at in ((slice(0, q_len), first, 0), (slice(2 * q_len, n), last, q_len)):
+        w, l, ob, lb = (t[at:at + q_len] for t in want)
+        kept = (out[rows] == 7).all(-1) & (lse[rows] == 7)
+        assert torch.all(kept[..., None] | ((out[rows].double() - w).abs() <= ob)) and torch.all(kept | ((lse[rows].double() - l).abs() <= lb))
