@@ -2,6 +2,7 @@
 // (include/pcd_kernels.h): argument checks, then one launch each.
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <climits>
 #include <cstdint>
@@ -56,6 +57,45 @@ int log2_page(int page) {
   for (int s = 4; s <= 7; ++s)
     if (page == 1 << s) return s;
   return -1;
+}
+
+// Rows of a view along one axis: n of them, `stride` bytes apart.
+struct Axis {
+  int64_t stride, n;
+};
+// Do two rows of `width` bytes meet, whose places differ by delta + sum d_i stride_i, |d_i| < n_i, one row being another
+// than itself (`other`: it is another view's) ?  Axes by falling stride: where each stride holds all that the axes
+// after it span, at most two d_i of an axis come near.
+bool rows_meet(__int128 delta, int64_t width, const Axis* ax, int k, bool other) {
+  if (k == 0) return other && delta < width && -delta < width;
+  __int128 span = width;  // of the axes after this one
+  for (int i = 1; i < k; ++i) span += static_cast<__int128>(ax[i].n - 1) * ax[i].stride;
+  const __int128 s = ax->stride, n = ax->n;
+  auto floor_div = [](__int128 a, __int128 b) { return a / b - (a % b < 0 ? 1 : 0); };
+  const __int128 lo = floor_div(-span - delta, s) + 1, hi = -(floor_div(delta - span, s) + 1);  // |delta + d s| < span
+  for (__int128 d = lo < 1 - n ? 1 - n : lo; d <= hi && d < n; ++d)
+    if (rows_meet(delta + d * s, width, ax + 1, k - 1, other || d != 0)) return true;
+  return false;
+}
+// Does some byte belong to two of a view's rows?
+bool rows_overlap(int64_t width, Axis* ax, int k) {
+  k = static_cast<int>(std::remove_if(ax, ax + k, [](const Axis& a) { return a.n <= 1; }) - ax);
+  std::sort(ax, ax + k, [](const Axis& a, const Axis& b) { return a.stride > b.stride; });
+  if (k > 0 && ax[k - 1].stride < 1) return true;
+  __int128 span = width;
+  for (int i = k - 1; i >= 0; --i) {
+    if (ax[i].stride < span) return rows_meet(0, width, ax, k, false);
+    span += static_cast<__int128>(ax[i].n - 1) * ax[i].stride;
+  }
+  return false;
+}
+bool rows_overlap(int64_t es, int64_t n, int64_t h, int64_t d, int64_t tok, int64_t head) {
+  Axis ax[2] = {{tok * es, n}, {head * es, h}};
+  return rows_overlap(d * es, ax, 2);
+}
+bool codes_overlap(const pcd::PagesView& c) {
+  Axis ax[3] = {{c.page_stride, c.n_pages}, {c.head_stride, c.Hkv}, {c.tok_stride, int64_t{1} << c.page_log2}};
+  return rows_overlap(c.dim, ax, 3);
 }
 
 // The cache as the kernels take it.
@@ -164,8 +204,7 @@ extern "C" int pcd_k_rope(const void* x, void* y, int dtype, int n_tok, int head
   PCD_REFUSE(!x || !y || !aligned(x, es) || !aligned(y, es) || !aligned(pos, 4), PCD_ERR_INVALID_ARG,
              "NULL or unaligned pointer");
   PCD_REFUSE(x_tok < 0 || x_head < 0 || y_tok < 0 || y_head < 0, PCD_ERR_INVALID_ARG, "negative stride");
-  PCD_REFUSE((heads > 1 && y_head < head_dim) || (n_tok > 1 && y_tok < head_dim), PCD_ERR_INVALID_ARG,
-             "strides of y overlap rows");
+  PCD_REFUSE(rows_overlap(es, n_tok, heads, head_dim, y_tok, y_head), PCD_ERR_INVALID_ARG, "strides of y overlap rows");
   PCD_REFUSE(!views_ok(x, y, es, n_tok, heads, head_dim, x_tok, x_head, y_tok, y_head), PCD_ERR_INVALID_ARG,
              "x and y overlap without being the same view");
   PCD_REFUSE(static_cast<int64_t>(n_tok) * head_dim >= (int64_t{1} << 31), PCD_ERR_INVALID_ARG,
@@ -193,6 +232,7 @@ extern "C" int pcd_k_kv_append_cols(const pcd_kv_pages* cache, const void* k, co
   PCD_REFUSE(k_tok < 0 || k_head < 0 || v_tok < 0 || v_head < 0, PCD_ERR_INVALID_ARG, "negative stride");
   PCD_REFUSE(cache->k == cache->v || cache->k_scale == cache->v_scale, PCD_ERR_INVALID_ARG,
              "cache: keys and values in one place");
+  PCD_REFUSE(codes_overlap(a.c), PCD_ERR_INVALID_ARG, "cache: strides overlap rows");
   a.k = k;
   a.v = v;
   a.dtype = dtype;
@@ -251,7 +291,7 @@ extern "C" int pcd_k_paged_attention_cols(const pcd_kv_pages* cache, const void*
   PCD_REFUSE(!q || !out || !aligned(q, 2) || !aligned(out, 2) || !aligned(lse, 4) || !aligned(dev_err, 4),
              PCD_ERR_INVALID_ARG, "NULL or unaligned pointer");
   PCD_REFUSE(q_tok < 0 || q_head < 0 || out_tok < 0 || out_head < 0, PCD_ERR_INVALID_ARG, "negative stride");
-  PCD_REFUSE((n_q_heads > 1 && out_head < a.c.dim) || (n_tok > 1 && out_tok < a.c.dim), PCD_ERR_INVALID_ARG,
+  PCD_REFUSE(rows_overlap(2, n_tok, n_q_heads, a.c.dim, out_tok, out_head), PCD_ERR_INVALID_ARG,
              "strides of out overlap rows");
   PCD_REFUSE(!views_ok(q, out, 2, n_tok, n_q_heads, a.c.dim, q_tok, q_head, out_tok, out_head), PCD_ERR_INVALID_ARG,
              "q and out overlap without being the same view");

@@ -188,7 +188,8 @@ int pcd_rope_freqs(int rot_dim, double theta, int scaling, double factor, double
  * else (i, i + rot_dim / 2).  transpose != 0 turns by -phi with the same amp:
  * the gradient of the rotation.  Token t is at pos[t], or base + t when pos is
  * NULL; any int32 position, negative ones included.  y may be x's own view;
- * another overlap is refused, and so is n_tok * head_dim of 2^31 and more. */
+ * another overlap is refused, as are strides that put two rows of y in one
+ * place and n_tok * head_dim of 2^31 and more. */
 int pcd_k_rope(const void* x, void* y, int dtype, int n_tok, int heads, int head_dim, int64_t x_tok, int64_t x_head,
                int64_t y_tok, int64_t y_head, const int64_t* freqs, int rot_dim, int interleaved, float amp,
                const int32_t* pos, int base, int transpose, void* stream);
@@ -234,7 +235,8 @@ typedef struct {
  * nearest even.  A NaN or infinity in a block's rows makes its scale so, and
  * all that is read from that block NaN.  A page that one call appends to
  * belongs to one sequence.  Nothing but the new tokens' pages is written.
- * Keys and values in one place are refused. */
+ * Strides that put two rows of the cache in one place are refused, and keys and
+ * values in one place. */
 int pcd_k_kv_append(const pcd_kv_pages* cache, const void* k, const void* v, int dtype, int64_t k_tok, int64_t k_head,
                     int64_t v_tok, int64_t v_head, const int32_t* q_off, const int32_t* kv_len, const int32_t* table,
                     int n_seq, int n_tok, int table_stride, const int64_t* freqs, int rot_dim, int interleaved,
@@ -258,7 +260,8 @@ int pcd_k_kv_append_cols(const pcd_kv_pages* cache, const void* k, const void* v
  * accumulated in fp32; codes enter the products exactly and a value's scale
  * joins the softmax weight before its rounding to fp16.  Keys of a page that
  * the table has out of range are not seen; a length beyond the table reads as
- * zero tokens.  `out` may be q's own view; another overlap is refused.
+ * zero tokens.  `out` may be q's own view; another overlap is refused, as are
+ * strides that put two of its rows in one place.
  * max_kv: the longest kv_len, as far as the host knows it; it sets how many
  * key ranges run side by side, not what is computed.  `scratch`: 16-byte
  * aligned, at least pcd_k_paged_attention_scratch_bytes (the same sizes, the

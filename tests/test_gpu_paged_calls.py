@@ -171,3 +171,44 @@ def test_attention_leaves_skipped_rows(paged, q_len, hint, dim, empty):  # noqa:
         w, l, ob, lb = (t[at:at + q_len] for t in want)
         kept = (out[rows] == 7).all(-1) & (lse[rows] == 7)
         assert torch.all(kept[..., None] | ((out[rows].double() - w).abs() <= ob)) and torch.all(kept | ((lse[rows].double() - l).abs() <= lb))
+
+
+# ------------------------------------------------------------------- odd places
+@pytest.mark.parametrize("strides", [(192, 128), (128, 192), (64, 200), (200, 64)])
+def test_outputs_that_interleave(paged, strides):  # noqa: F811
+    """Rows of an output that lie between one another without meeting, not all
+    of them one axis within the other."""
+    n, heads, dim = 3, 2, 64
+    x = torch.randn(n, heads, dim, generator=gen(5), device="cuda").half()
+    freqs = paged.pcd_rope_freqs(64, 1e6)[0].cuda()
+    buf = torch.full((2048,), 7.0, dtype=torch.float16, device="cuda")
+    out = buf.as_strided((n, heads, dim), (*strides, 1))
+    assert torch.equal(paged.pcd_k_rope(x, freqs, out=out), paged.pcd_k_rope(x, freqs))
+    q, *rest = attend_case("e4m3", "f16", 16, dim, heads, 1, [n], [90], 3)
+    assert torch.equal(paged.pcd_k_paged_attention(q, *rest, out=out), paged.pcd_k_paged_attention(q, *rest))
+    untouched = torch.ones_like(buf, dtype=torch.bool)
+    untouched.as_strided((n, heads, dim), (*strides, 1))[:] = False
+    assert torch.all(buf[untouched] == 7)
+
+
+def test_append_to_caches_in_odd_places(paged):  # noqa: F811
+    """Caches cut out of pools that hold other things between their rows, or
+    whose pages and heads lie between one another."""
+    new, old = [40, 17], [0, 30]
+    table, kc, vc, ks, vs, k, v, q_off, kv_len, n = append_case("int8", "f16", 16, 64, 2, new, old, 0, False)
+    pool = kc.shape[0]
+    want = [t.clone() for t in (kc, vc, ks, vs)]
+    paged.pcd_k_kv_append(k, v, *want, q_off, kv_len, table)
+
+    def check(kd, vd):
+        kd.copy_(kc), vd.copy_(vc)
+        s = [ks.clone(), vs.clone()]
+        paged.pcd_k_kv_append(k, v, kd, vd, *s, q_off, kv_len, table)
+        assert all(torch.equal(a, b) for a, b in zip((kd, vd, *s), want))
+
+    both = torch.zeros(pool, 2, 16, 2, 128, dtype=torch.int8, device="cuda")  # [page][k, v][slot][head], wide rows
+    check(*(both[:, i, :, :, 64:].transpose(1, 2) for i in range(2)))
+    pair = torch.zeros(pool, 2, 16, 128, dtype=torch.int8, device="cuda")  # keys and values side by side in a row
+    check(pair[..., :64], pair[..., 64:])
+    flat = torch.zeros(2, 16 * 192 * pool, dtype=torch.int8, device="cuda")  # slots of three heads' width, heads between
+    check(*(f.as_strided((pool, 2, 16, 64), (16 * 192, 64, 192, 1)) for f in flat))

@@ -5,7 +5,7 @@ import ctypes
 
 import pytest
 
-from test_paged_refusals import BASE, INVALID, append, attend, lib, pages  # noqa: F401
+from test_paged_refusals import BASE, INVALID, append, attend, lib, pages, rope  # noqa: F401
 
 
 # ------------------------------------------------------------- table slices
@@ -24,3 +24,22 @@ def test_table_slices_refused(lib, stride, width):  # noqa: F811
     for call in (append_cols, attend_cols):
         assert call(lib, stride, width) == INVALID and lib.pcd_last_error()
         assert call(lib, 4, 3, n=0) == 0
+
+
+# -------------------------------------------------------- rows that share a place
+@pytest.mark.parametrize("tok,head,heads", [(64, 64, 2), (128, 64, 3), (64, 128, 2), (96, 64, 2), (100, 164, 2), (160, 96, 3), (128, 190, 2)])
+def test_outputs_whose_rows_overlap(lib, tok, head, heads):  # noqa: F811
+    """Each stride alone holds a row, together they put two rows in one place."""
+    assert rope(lib, yt=tok, yh=head, heads=heads, xt=64 * heads, y=1 << 40) == INVALID
+    assert b"strides of y overlap" in lib.pcd_last_error()
+    assert attend(lib, ot=tok, oh=head, hq=2 * heads, out=1 << 40) == INVALID
+    assert b"strides of out overlap" in lib.pcd_last_error()
+
+
+@pytest.mark.parametrize("kw", [
+    dict(page_stride=64), dict(page_stride=1024), dict(head_stride=64), dict(head_stride=512), dict(token_stride=128),
+    dict(page_stride=1024 + 16), dict(page_stride=64, head_stride=64 * 8), dict(page_stride=128, head_stride=64, token_stride=192),
+])
+def test_append_refuses_caches_whose_rows_overlap(lib, kw):  # noqa: F811
+    assert append(lib, pages(**kw)) == INVALID
+    assert b"cache: strides overlap" in lib.pcd_last_error()
