@@ -77,10 +77,15 @@ bool rows_meet(__int128 delta, int64_t width, const Axis* ax, int k, bool other)
     if (rows_meet(delta + d * s, width, ax + 1, k - 1, other || d != 0)) return true;
   return false;
 }
-// Does some byte belong to two of a view's rows?
-bool rows_overlap(int64_t width, Axis* ax, int k) {
+// The axes of more than one row, by falling stride; returns how many.
+int order_axes(Axis* ax, int k) {
   k = static_cast<int>(std::remove_if(ax, ax + k, [](const Axis& a) { return a.n <= 1; }) - ax);
   std::sort(ax, ax + k, [](const Axis& a, const Axis& b) { return a.stride > b.stride; });
+  return k;
+}
+// Does some byte belong to two of a view's rows?
+bool rows_overlap(int64_t width, Axis* ax, int k) {
+  k = order_axes(ax, k);
   if (k > 0 && ax[k - 1].stride < 1) return true;
   __int128 span = width;
   for (int i = k - 1; i >= 0; --i) {
@@ -96,6 +101,15 @@ bool rows_overlap(int64_t es, int64_t n, int64_t h, int64_t d, int64_t tok, int6
 bool codes_overlap(const pcd::PagesView& c) {
   Axis ax[3] = {{c.page_stride, c.n_pages}, {c.head_stride, c.Hkv}, {c.tok_stride, int64_t{1} << c.page_log2}};
   return rows_overlap(c.dim, ax, 3);
+}
+// Do keys and values, or their scales, share a byte?  (Of a cache whose rows share none.)
+bool keys_meet_values(const pcd::PagesView& c) {
+  const int64_t scales = static_cast<int64_t>(c.n_pages) * c.Hkv;
+  if (c.ks < c.vs + scales && c.vs < c.ks + scales) return true;
+  Axis ax[3] = {{c.page_stride, c.n_pages}, {c.head_stride, c.Hkv}, {c.tok_stride, int64_t{1} << c.page_log2}};
+  const int k = order_axes(ax, 3);
+  const __int128 delta = reinterpret_cast<intptr_t>(c.v) - reinterpret_cast<intptr_t>(c.k);
+  return rows_meet(delta, c.dim, ax, k, true);
 }
 
 // The cache as the kernels take it.
@@ -230,9 +244,8 @@ extern "C" int pcd_k_kv_append_cols(const pcd_kv_pages* cache, const void* k, co
   PCD_REFUSE(!k || !v || !aligned(k, es) || !aligned(v, es) || !aligned(pos, 4) || !aligned(dev_err, 4),
              PCD_ERR_INVALID_ARG, "NULL or unaligned pointer");
   PCD_REFUSE(k_tok < 0 || k_head < 0 || v_tok < 0 || v_head < 0, PCD_ERR_INVALID_ARG, "negative stride");
-  PCD_REFUSE(cache->k == cache->v || cache->k_scale == cache->v_scale, PCD_ERR_INVALID_ARG,
-             "cache: keys and values in one place");
   PCD_REFUSE(codes_overlap(a.c), PCD_ERR_INVALID_ARG, "cache: strides overlap rows");
+  PCD_REFUSE(keys_meet_values(a.c), PCD_ERR_INVALID_ARG, "cache: keys and values in one place");
   a.k = k;
   a.v = v;
   a.dtype = dtype;

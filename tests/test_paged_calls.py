@@ -43,3 +43,15 @@ def test_outputs_whose_rows_overlap(lib, tok, head, heads):  # noqa: F811
 def test_append_refuses_caches_whose_rows_overlap(lib, kw):  # noqa: F811
     assert append(lib, pages(**kw)) == INVALID
     assert b"cache: strides overlap" in lib.pcd_last_error()
+
+
+@pytest.mark.parametrize("kw", [
+    dict(v=BASE + 16), dict(v=BASE + 48), dict(v=BASE - 48), dict(v=BASE + 1024), dict(v=BASE + 2048 * 7 + 1024), dict(v=BASE - 2048 * 7),
+    dict(token_stride=128, head_stride=2048, page_stride=4096, v=BASE + 48), dict(v=BASE + 2048 * 8 - 16),
+    dict(v_scale=BASE + 4), dict(v_scale=BASE + 4 * 15), dict(v_scale=BASE - 4 * 15),
+    dict(page_size=32, n_pages=3, n_kv_heads=5, head_stride=64, token_stride=320, page_stride=320 * 32, v=BASE + 2 * 10240 + 320 * 31 + 64 * 4 + 48),
+])
+def test_append_refuses_keys_over_values(lib, kw):  # noqa: F811
+    """Keys and values, or their scales, that share some places."""
+    assert append(lib, pages(**kw)) == INVALID
+    assert b"one place" in lib.pcd_last_error()
