@@ -147,11 +147,17 @@ int view_seqs(const int32_t* q_off, const int32_t* kv_len, const int32_t* table,
 }
 
 // May a kernel that reads the rows of x and then writes the same rows of y run
-// on these two views?  They are the same view, or share no element.
-bool views_ok(const void* x, const void* y, int64_t es, int n, int h, int d, int64_t xt, int64_t xh, int64_t yt,
-                     int64_t yh) {
-  if (x == y && (xt == yt || n <= 1) && (xh == yh || h <= 1)) return true;
+// on these two views (no two rows of y meet)?  They are the same view, or share
+// no byte; that is decided exactly where their strides are equal, else by the
+// span of their rows within a common token stride, or of all.
+bool views_ok(const void* x, const void* y, int64_t es, int64_t n, int64_t h, int64_t d, int64_t xt, int64_t xh, int64_t yt,
+              int64_t yh) {
   const int64_t xa = reinterpret_cast<int64_t>(x), ya = reinterpret_cast<int64_t>(y);
+  if ((xt == yt || n <= 1) && (xh == yh || h <= 1)) {
+    Axis ax[2] = {{yt * es, n}, {yh * es, h}};
+    const int k = order_axes(ax, 2);
+    return x == y || !rows_meet(ya - xa, d * es, ax, k, true);
+  }
   const int64_t xs = ((n - 1) * xt + (h - 1) * xh + d) * es, ys = ((n - 1) * yt + (h - 1) * yh + d) * es;
   if (xa + xs <= ya || ya + ys <= xa) return true;
   if (xt != yt || xt <= 0) return false;

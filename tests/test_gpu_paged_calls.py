@@ -212,3 +212,20 @@ def test_append_to_caches_in_odd_places(paged):  # noqa: F811
     check(pair[..., :64], pair[..., 64:])
     flat = torch.zeros(2, 16 * 192 * pool, dtype=torch.int8, device="cuda")  # slots of three heads' width, heads between
     check(*(f.as_strided((pool, 2, 16, 64), (16 * 192, 64, 192, 1)) for f in flat))
+
+
+def test_output_beside_the_input(paged):  # noqa: F811
+    """The output in the other half of the input's heads, and in every second
+    token's rows: places of their own, though the rows lie between one another."""
+    freqs = paged.pcd_rope_freqs(64, 1e6)[0].cuda()
+    q, *rest = attend_case("int8", "f16", 16, 64, 4, 2, [9, 3], [90, 30], 3)
+    n = q.shape[0]
+    for shape, cut in (((n, 4, 128), lambda b, i: b[..., 64 * i:64 * i + 64]), ((2 * n, 4, 64), lambda b, i: b[i::2]),
+                       ((n, 8, 64), lambda b, i: b[:, i::2]), ((n, 4, 160), lambda b, i: b[..., 80 * i:80 * i + 64])):
+        for i in (0, 1):
+            buf = torch.full(shape, 7.0, dtype=q.dtype, device="cuda")
+            x, y = cut(buf, i), cut(buf, 1 - i)
+            x.copy_(q)
+            assert torch.equal(paged.pcd_k_rope(x, freqs, out=y), paged.pcd_k_rope(q, freqs)) and torch.equal(x, q)
+            assert torch.equal(paged.pcd_k_paged_attention(x, *rest, out=y), paged.pcd_k_paged_attention(q, *rest))
+            assert torch.equal(x, q)

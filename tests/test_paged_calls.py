@@ -55,3 +55,12 @@ def test_append_refuses_keys_over_values(lib, kw):  # noqa: F811
     """Keys and values, or their scales, that share some places."""
     assert append(lib, pages(**kw)) == INVALID
     assert b"one place" in lib.pcd_last_error()
+
+
+@pytest.mark.parametrize("kw", [dict(y=BASE + 2 * 32), dict(y=BASE + 2 * 128), dict(y=BASE - 2 * 64), dict(y=BASE + 2 * 64, heads=1),
+                                dict(xt=256, yt=256, xh=128, yh=128, y=BASE + 2 * 48), dict(xt=256, yt=256, xh=128, yh=128, y=BASE + 2 * 208)])
+def test_views_of_equal_strides_that_meet(lib, kw):  # noqa: F811
+    if kw.get("heads") == 1:
+        kw = dict(kw, xt=64, yt=64)
+    assert rope(lib, **kw) == INVALID
+    assert b"overlap without" in lib.pcd_last_error()
