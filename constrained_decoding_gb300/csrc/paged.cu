@@ -52,7 +52,7 @@ __global__ void __launch_bounds__(256) rope_kernel(RopeKArgs a, unsigned units, 
   }
   const int pair = static_cast<int>(u) * kPairs;
   const int d = static_cast<int>(u) * kN, half = a.rope.rot / 2;
-  const int p = a.pos ? a.pos[t] : a.base + t;
+  const int64_t p = a.pos ? a.pos[t] : static_cast<int64_t>(a.base) + t;
   float c[kPairs], s[kPairs];
 #pragma unroll
   for (int i = 0; i < kPairs; ++i) {

@@ -29,8 +29,8 @@ __device__ __forceinline__ __nv_bfloat16 from_f<__nv_bfloat16>(float x) { return
 // cos and sin of position p at F turns (2^-64) per position: p F wraps at
 // whole turns, so the product is exact; its top 32 bits are the angle in
 // (-1/2, 1/2] turns to 2^-32, under fp32's own rounding of it.
-__device__ __forceinline__ void turn(int p, int64_t F, float* c, float* s) {
-  const uint64_t phase = static_cast<uint64_t>(static_cast<int64_t>(p)) * static_cast<uint64_t>(F);
+__device__ __forceinline__ void turn(int64_t p, int64_t F, float* c, float* s) {
+  const uint64_t phase = static_cast<uint64_t>(p) * static_cast<uint64_t>(F);
   sincospif(static_cast<float>(static_cast<int32_t>(phase >> 32)) * 4.656612873077393e-10f /* 2^-31: half turns */, s, c);
 }
 

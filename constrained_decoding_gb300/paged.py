@@ -114,6 +114,8 @@ def pcd_k_rope(x, freqs, pos=None, *, base: int = 0, interleaved: bool = False, 
     n, heads, dim = shape
     xs = _rows(x, dev, shape, dtype, "x")
     f, rot = _rope(freqs, dev, dim)
+    if not -0x80000000 <= base <= 0x7fffffff:
+        raise ValueError("base: a 32-bit integer")
     if out is None:
         out = torch.empty(shape, dtype=dtype, device=x.device)
         ys = (heads * dim, dim)

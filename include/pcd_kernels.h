@@ -187,9 +187,9 @@ int pcd_rope_freqs(int rot_dim, double theta, int scaling, double factor, double
  * b cos phi + a sin phi); pairs are channels (2i, 2i + 1) when `interleaved`,
  * else (i, i + rot_dim / 2).  transpose != 0 turns by -phi with the same amp:
  * the gradient of the rotation.  Token t is at pos[t], or base + t when pos is
- * NULL; any int32 position, negative ones included.  y may be x's own view;
- * another overlap is refused, as are strides that put two rows of y in one
- * place and n_tok * head_dim of 2^31 and more. */
+ * NULL; any int32 pos and base, negative ones included (base + t may pass
+ * 2^31).  y may be x's own view; another overlap is refused, as are strides that
+ * put two rows of y in one place and n_tok * head_dim of 2^31 and more. */
 int pcd_k_rope(const void* x, void* y, int dtype, int n_tok, int heads, int head_dim, int64_t x_tok, int64_t x_head,
                int64_t y_tok, int64_t y_head, const int64_t* freqs, int rot_dim, int interleaved, float amp,
                const int32_t* pos, int base, int transpose, void* stream);
@@ -199,8 +199,9 @@ int pcd_k_rope(const void* x, void* y, int dtype, int n_tok, int heads, int head
  * token_stride of `k` and `v` (strides and bases multiples of 16 bytes,
  * token_stride at most 2^24), so both [page][head][slot] and
  * [page][slot][head] orders serve.  A page holds page_size (16, 32, 64 or
- * 128) consecutive tokens of one sequence; each (page, KV head) has one scale in k_scale / v_scale [n_pages][n_kv_heads],
- * fp32: value = code * scale.  head_dim 64 or 128. */
+ * 128) consecutive tokens of one sequence; each (page, KV head) has one scale
+ * in k_scale / v_scale [n_pages][n_kv_heads], fp32: value = code * scale.
+ * head_dim 64 or 128. */
 #define PCD_KV_E4M3 1 /* 8-bit floats, 4 exponent bits; scales are powers of two when written here, and no code is NaN */
 #define PCD_KV_INT8 2 /* signed integers, -127 .. 127 */
 typedef struct {

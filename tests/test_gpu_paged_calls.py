@@ -229,3 +229,25 @@ def test_output_beside_the_input(paged):  # noqa: F811
             assert torch.equal(paged.pcd_k_rope(x, freqs, out=y), paged.pcd_k_rope(q, freqs)) and torch.equal(x, q)
             assert torch.equal(paged.pcd_k_paged_attention(x, *rest, out=y), paged.pcd_k_paged_attention(q, *rest))
             assert torch.equal(x, q)
+
+
+@pytest.mark.parametrize("base", [2 ** 31 - 4, 2 ** 31 - 1, -2 ** 31, -5])
+@pytest.mark.parametrize("inter", [False, True])
+def test_rope_base_at_the_ends(paged, base, inter):  # noqa: F811
+    """Positions base + row that pass 2^31, or start at -2^31."""
+    n = 9
+    x = torch.randn(n, 3, 64, generator=gen(2), device="cuda")
+    freqs, _ = paged.pcd_rope_freqs(64, 1e4)
+    y = paged.pcd_k_rope(x, freqs.cuda(), base=base, interleaved=inter)
+    for t in range(n):
+        turns = torch.tensor([((base + t) * int(f)) % 2 ** 64 / 2 ** 64 for f in freqs.tolist()], dtype=torch.float64, device="cuda")
+        want, err = R.rotate(x[t:t + 1], torch.ones(1, device="cuda"), turns * 2 * math.pi, inter)
+        assert torch.all((y[t:t + 1].double() - want).abs() <= err + want.abs() * R.HALF[x.dtype] * 1.001)
+
+
+def test_rope_base_refused(paged):  # noqa: F811
+    x = torch.zeros(2, 1, 64, device="cuda")
+    freqs = paged.pcd_rope_freqs(64, 1e4)[0].cuda()
+    for base in (2 ** 31, -2 ** 31 - 1, 2 ** 32, 2 ** 70):
+        with pytest.raises(ValueError):
+            paged.pcd_k_rope(x, freqs, base=base)
