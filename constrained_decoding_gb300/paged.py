@@ -38,6 +38,7 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 _current_device = torch.cuda.current_device
 _int32, _int64, _float32 = torch.int32, torch.int64, torch.float32
+_INT = 0x7fffffff  # the library's sizes are C ints, which ctypes would fill with the low 32 bits of a larger one
 
 # The checks below run on every call of a latency-bound loop, so a message is
 # put together only when it is raised.
@@ -69,6 +70,8 @@ def _rows(t, dev: int, shape, dtype, what: str):
     st = t.stride()
     if t.get_device() != dev or t.shape != shape or t.dtype is not dtype or (st[2] != 1 and shape[2] != 1):
         raise ValueError(f"{what}: {list(shape)} of {dtype} on cuda:{dev}, channels contiguous")
+    if shape[0] > _INT or shape[1] > _INT:
+        raise ValueError(f"{what}: under 2^31 rows and heads")
     return st
 
 
@@ -152,6 +155,8 @@ def _table(table, n_seq: int, dev: int):
     if (table.dtype is not _int32 or table.get_device() != dev or len(shape) != 2 or shape[0] != n_seq or
             (st[1] != 1 and shape[1] > 1) or (st[0] < shape[1] and n_seq > 1)):
         raise ValueError(f"table: int32 [{n_seq}, pages] on cuda:{dev}, rows contiguous")
+    if n_seq > _INT or shape[1] > _INT or (st[0] > _INT and n_seq > 1):
+        raise ValueError("table: under 2^31 sequences and pages")
     return table.data_ptr(), st[0] if n_seq > 1 else shape[1], shape[1]
 
 
@@ -181,6 +186,8 @@ def pcd_k_kv_append(k, v, k_cache, v_cache, k_scale, v_scale, q_off, kv_len, tab
 
 def pcd_k_paged_attention_scratch_bytes(n_tok: int, n_seq: int, n_q_heads: int, n_kv_heads: int, head_dim: int,
                                         max_kv: int) -> int:
+    if max(n_tok, n_seq, n_q_heads, n_kv_heads, head_dim) > _INT:
+        raise ValueError("sizes under 2^31")
     return int(_lib.pcd_k_paged_attention_scratch_bytes(n_tok, n_seq, n_q_heads, n_kv_heads, head_dim, max_kv))
 
 

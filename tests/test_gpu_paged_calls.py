@@ -251,3 +251,21 @@ def test_rope_base_refused(paged):  # noqa: F811
     for base in (2 ** 31, -2 ** 31 - 1, 2 ** 32, 2 ** 70):
         with pytest.raises(ValueError):
             paged.pcd_k_rope(x, freqs, base=base)
+
+
+def test_sizes_beyond_c_ints(paged):  # noqa: F811
+    """More rows than a C int counts are refused, not taken by their low bits."""
+    freqs = paged.pcd_rope_freqs(2, 1e4)[0].cuda()
+    for n in (2 ** 31, 2 ** 32 + 1):
+        with pytest.raises(ValueError):
+            paged.pcd_k_rope(torch.zeros(1, 1, 2, device="cuda").expand(n, 1, 2), freqs)
+        with pytest.raises(ValueError):
+            paged.pcd_k_rope(torch.zeros(1, 1, 2, device="cuda").expand(1, n, 2), freqs)
+        q, *cache, q_off, kv_len, table = attend_case("int8", "f16", 16, 64, 2, 2, [1], [20], 3)
+        many = q.expand(n, 2, 64)
+        with pytest.raises(ValueError):
+            paged.pcd_k_paged_attention(many, *cache, q_off, kv_len, table)
+        with pytest.raises(ValueError):
+            paged.pcd_k_kv_append(many, many, *cache, q_off, kv_len, table)
+        with pytest.raises(ValueError):
+            paged.pcd_k_paged_attention_scratch_bytes(n, 1, 2, 2, 64, 100)
