@@ -16,6 +16,12 @@ the library itself refuses raises PCDError.  A cache is two tensors [pages,
 KV heads, page size, head dim] of torch.float8_e4m3fn or torch.int8 (any strides
 that keep channels contiguous, the same for both) and two float32 scales
 [pages, KV heads].
+
+None of the calls records a gradient, so rows that require one are refused
+unless gradients are off (torch.no_grad(), detach()); in a backward pass of
+one's own, pcd_k_rope(..., transpose=True) is the rotation's gradient.  Writes to
+`out`, the cache and its scales do not count as in-place changes that autograd
+knows of: what it has saved must not be overwritten.
 """
 from __future__ import annotations
 
@@ -70,6 +76,8 @@ def _rows(t, dev: int, shape, dtype, what: str):
     st = t.stride()
     if t.get_device() != dev or t.shape != shape or t.dtype is not dtype or (st[2] != 1 and shape[2] != 1):
         raise ValueError(f"{what}: {list(shape)} of {dtype} on cuda:{dev}, channels contiguous")
+    if t.requires_grad and torch.is_grad_enabled():
+        raise ValueError(f"{what}: requires a gradient, which this call does not record")
     if shape[0] > _INT or shape[1] > _INT:
         raise ValueError(f"{what}: under 2^31 rows and heads")
     return st

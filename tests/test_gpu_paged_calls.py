@@ -269,3 +269,28 @@ def test_sizes_beyond_c_ints(paged):  # noqa: F811
             paged.pcd_k_kv_append(many, many, *cache, q_off, kv_len, table)
         with pytest.raises(ValueError):
             paged.pcd_k_paged_attention_scratch_bytes(n, 1, 2, 2, 64, 100)
+
+
+def test_rows_that_require_a_gradient(paged):  # noqa: F811
+    """No call records a gradient: rows that want one are refused, and taken
+    detached or where gradients are off."""
+    freqs = paged.pcd_rope_freqs(64, 1e6)[0].cuda()
+    q, *cache, q_off, kv_len, table = attend_case("int8", "f16", 16, 64, 2, 2, [3], [20], 3)
+    want = paged.pcd_k_rope(q, freqs), paged.pcd_k_paged_attention(q, *cache, q_off, kv_len, table)
+    leaf = q.clone().requires_grad_()
+    rows = leaf * 1.0
+    for x in (leaf, rows):
+        with pytest.raises(ValueError, match="gradient"):
+            paged.pcd_k_rope(x, freqs)
+        with pytest.raises(ValueError, match="gradient"):
+            paged.pcd_k_rope(q, freqs, out=x)
+        with pytest.raises(ValueError, match="gradient"):
+            paged.pcd_k_paged_attention(x, *cache, q_off, kv_len, table)
+        for k, v in ((x, q), (q, x)):
+            with pytest.raises(ValueError, match="gradient"):
+                paged.pcd_k_kv_append(k, v, *cache, q_off, kv_len, table)
+        assert torch.equal(paged.pcd_k_rope(x.detach(), freqs), want[0])
+        with torch.no_grad():
+            assert torch.equal(paged.pcd_k_paged_attention(x, *cache, q_off, kv_len, table), want[1])
+    with torch.inference_mode():
+        assert torch.equal(paged.pcd_k_rope(leaf, freqs), want[0])
