@@ -200,7 +200,8 @@ extern "C" int pcd_rope_freqs(int rot_dim, double theta, int scaling, double fac
       const double turns = orig_len * f0 / kTwoPi;
       stretched = 1.0 - std::fmin(std::fmax((turns - lo_turns) / (hi_turns - lo_turns), 0.0), 1.0);
     } else if (scaling == PCD_ROPE_RAMP) {
-      stretched = std::fmin(std::fmax((i - lo) / std::fmax(hi - lo, 1e-3), 0.0), 1.0);
+      // (hi below 0: the length is so short that even the first pair turns fewer than lo_turns times)
+      stretched = hi > 0.0 ? std::fmin(std::fmax((i - lo) / std::fmax(hi - lo, 1e-3), 0.0), 1.0) : 1.0;
     }
     const double f = stretched > 0.0 ? f0 / factor * stretched + f0 * (1.0 - stretched) : f0;
     const double turns = f / kTwoPi;  // < 1/6: theta > 1 and factor >= 1

@@ -64,3 +64,29 @@ def test_views_of_equal_strides_that_meet(lib, kw):  # noqa: F811
         kw = dict(kw, xt=64, yt=64)
     assert rope(lib, **kw) == INVALID
     assert b"overlap without" in lib.pcd_last_error()
+
+
+# ------------------------------------------------------------------ frequencies
+@pytest.mark.parametrize("scaling", ["bands", "ramp"])
+@pytest.mark.parametrize("orig,lo,hi", [(1.0, 1.0, 32.0), (6.0, 1.0, 4.0), (40.0, 8.0, 9.0), (6.3, 1.0, 32.0), (1e9, 1.0, 32.0), (1e300, 1.0, 2.0)])
+def test_frequencies_at_the_ends_of_the_scalings(lib, scaling, orig, lo, hi):  # noqa: F811
+    """Pairs that turn at least hi times over the length stay, those that turn
+    at most lo times are divided by the factor, for lengths so short that even
+    the first pair is among these and so long that all stay."""
+    import math
+
+    from constrained_decoding_gb300 import paged
+    rot, theta, factor = 32, 1e4, 8.0
+    freqs, _ = paged.pcd_rope_freqs(rot, theta, scaling, factor, orig, lo, hi)
+    for i, v in enumerate(freqs.tolist()):
+        f = theta ** (-2 * i / rot)
+        turns = orig * f / (2 * math.pi)
+        got = (v % 2 ** 64) / 2 ** 64 * 2 * math.pi
+        # the ramp's ends are rounded outwards to whole pairs: only pairs beyond those are at an end for sure
+        step = theta ** (2 / rot) if scaling == "ramp" and turns < orig / (2 * math.pi) else 1.0
+        if turns >= hi * step:
+            assert got == pytest.approx(f, rel=1e-12), i
+        elif turns * step <= lo:
+            assert got == pytest.approx(f / factor, rel=1e-12), i
+        else:
+            assert f / factor * (1 - 1e-12) <= got <= f * (1 + 1e-12), i
