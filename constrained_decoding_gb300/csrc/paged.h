@@ -86,6 +86,7 @@ struct PagedAttnArgs {
   float2* part_ml;
   int2* part_at;
   int* err;
+  uint64_t wait_ns;  // limit of a pipeline's waits
 };
 void plan_paged_attention(int n_tok, int n_seq, int G, int Hkv, int64_t max_kv, int sms, PagedPlan* p);
 int launch_paged_attention(const PagedAttnArgs& a, cudaStream_t s);

@@ -6,6 +6,7 @@
 #include <cmath>
 #include <climits>
 #include <cstdint>
+#include <cstdlib>
 
 #include "paged.h"
 #include "pcd.h"
@@ -43,6 +44,15 @@ int launched(int r) {
   if (r == 0) return PCD_OK;
   const cudaError_t e = cudaGetLastError();
   return pcd::set_error(PCD_ERR_CUDA, e == cudaSuccess ? "kernel launch failed" : cudaGetErrorString(e));
+}
+
+// Limit of a pipeline's waits: 2 s, or PCD_WAIT_LIMIT_MS as the process's first call finds it.
+uint64_t wait_limit_ns() {
+  static const uint64_t ns = [] {
+    const char* ms = std::getenv("PCD_WAIT_LIMIT_MS");
+    return ms ? static_cast<uint64_t>(std::atof(ms) * 1e6) : uint64_t{2000000000};
+  }();
+  return ns;
 }
 
 int check_rope(const pcd::RopeSpec& r, int dim) {
@@ -325,6 +335,7 @@ extern "C" int pcd_k_paged_attention_cols(const pcd_kv_pages* cache, const void*
   a.x_tok = q_tok, a.x_head = q_head, a.out_tok = out_tok, a.out_head = out_head;
   a.scale_log2 = scale * 1.4426950408889634f;
   a.err = dev_err;
+  a.wait_ns = wait_limit_ns();
   pcd::plan_paged_attention(n_tok, n_seq, a.G, a.c.Hkv, max_kv, device_sms(), &a.plan);
   const int64_t need = attn_scratch(n_tok, n_q_heads, a.c.dim, a.plan);
   if (need > 0) {

@@ -55,7 +55,6 @@ static_assert(kRowsCta == kTileRows, "rows of an item");
 constexpr int kBlock = 128;       // keys of a block (MMA N of S, K of P V)
 constexpr int kHalf = kTile * 128;  // bytes of 64 channels x 128 rows, one 128-byte swizzled row each
 constexpr float kSlackTc = 7.f;
-constexpr uint64_t kWaitNs = 2000000000ull;
 
 template <int D>
 struct TileCfg {
@@ -263,8 +262,8 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
       };
       // turn[t] completes once before each of the tile's turns; the first tile's first turn is free
       const int step = alt ? 2 : 1, i0 = alt ? t : 0;
-      bool ok = mbar_wait(&k_full[i0], 0, kWaitNs) && mbar_wait(&q_full[alt ? 0 : t], 0, kWaitNs) &&
-                (t == 0 || alt || C::kOwnP || mbar_wait(&turn[1], 0, kWaitNs));
+      bool ok = mbar_wait(&k_full[i0], 0, a.wait_ns) && mbar_wait(&q_full[alt ? 0 : t], 0, a.wait_ns) &&
+                (t == 0 || alt || C::kOwnP || mbar_wait(&turn[1], 0, a.wait_ns));
       ok = __all_sync(0xffffffffu, ok);
       if (ok) issue_s(i0);
       const uint32_t dP = C::kOwnP ? tb + C::kColP + t * C::kStepP : dS;
@@ -274,15 +273,15 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
         auto next_s = [&](uint64_t* freed) {
           const int in = i + step;
           if (in >= nb) return;
-          ok = mbar_wait(&k_full[in & 1], static_cast<uint32_t>((in >> 1) & 1), kWaitNs) && mbar_wait(freed, par, kWaitNs);
+          ok = mbar_wait(&k_full[in & 1], static_cast<uint32_t>((in >> 1) & 1), a.wait_ns) && mbar_wait(freed, par, a.wait_ns);
           ok = __all_sync(0xffffffffu, ok && !*abort_flag);
           if (ok) issue_s(in & 1);
         };
         if (C::kOwnP) next_s(&s_free[t]);
         if (!ok) break;
-        ok = mbar_wait(&v_full[st], static_cast<uint32_t>((i >> 1) & 1), kWaitNs) &&
-             (!two || C::kOwnP || mbar_wait(&turn[t], static_cast<uint32_t>((i + t) & 1), kWaitNs)) &&
-             mbar_wait(&p_full[t], par, kWaitNs);
+        ok = mbar_wait(&v_full[st], static_cast<uint32_t>((i >> 1) & 1), a.wait_ns) &&
+             (!two || C::kOwnP || mbar_wait(&turn[t], static_cast<uint32_t>((i + t) & 1), a.wait_ns)) &&
+             mbar_wait(&p_full[t], par, a.wait_ns);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after_sync();
@@ -342,7 +341,7 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
 #pragma unroll 1
         for (int kv = 0; kv < 2 && ok; ++kv) {
           const int before = i - (alt ? 2 : 1);  // the block whose codes were here
-          if (before >= 0) ok = mbar_wait(&raw_free[raw_bar(before, kv)], raw_par(before), kWaitNs);
+          if (before >= 0) ok = mbar_wait(&raw_free[raw_bar(before, kv)], raw_par(before), a.wait_ns);
           ok = __all_sync(0xffffffffu, ok && !*abort_flag);
           if (!ok) break;
           const uint8_t* base = kv ? a.c.v : a.c.k;
@@ -401,8 +400,8 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
       const int live = min(kBlock, len - (b0 + i) * kBlock);  // rows behind the last token read as zeros
 #pragma unroll 1
       for (int kv = 0; kv < 2; ++kv) {
-        ok = mbar_wait(&raw_full[raw_bar(i, kv)], raw_par(i), kWaitNs);
-        if (ok && i >= 2) ok = mbar_wait(kv ? &v_free[st] : &k_free[st], static_cast<uint32_t>(((i - 2) >> 1) & 1), kWaitNs);
+        ok = mbar_wait(&raw_full[raw_bar(i, kv)], raw_par(i), a.wait_ns);
+        if (ok && i >= 2) ok = mbar_wait(kv ? &v_free[st] : &k_free[st], static_cast<uint32_t>(((i - 2) >> 1) & 1), a.wait_ns);
         ok = __all_sync(0xffffffffu, ok && !*abort_flag);
         if (!ok) break;
         const bool whole = whole_block[i & 7] != 0;
@@ -530,7 +529,7 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
       const int wmin = __reduce_min_sync(0xffffffffu, vis);  // keys that every row of the warp sees
       int n = 0;  // blocks done
       for (int i = alt ? t : 0; i < nb; i += alt ? 2 : 1, ++n) {
-        ok = __all_sync(0xffffffffu, mbar_wait(&s_full[t], static_cast<uint32_t>(n & 1), kWaitNs) && !*abort_flag);
+        ok = __all_sync(0xffffffffu, mbar_wait(&s_full[t], static_cast<uint32_t>(n & 1), a.wait_ns) && !*abort_flag);
         if (!ok) break;
         tc_fence_after_sync();
         float s[kBlock];
@@ -578,7 +577,7 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
           const float m_new = fmaxf(m_ref, mx);
           const float f = m_ref == -INFINITY ? 0.f : ex2_approx(m_ref - m_new);
           if (n > 0) {
-            ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[t], static_cast<uint32_t>((n - 1) & 1), kWaitNs));
+            ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[t], static_cast<uint32_t>((n - 1) & 1), a.wait_ns));
             if (!ok) break;
             tc_fence_after_sync();
 #pragma unroll 1
@@ -618,7 +617,7 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
             l = fmaf(sum.x + sum.y, plain || vis > j0 + 16 * g ? k.z : 0.f, l);
           }
           if (C::kOwnP && q2 == 0 && n > 0) {  // the block before has left the weights' columns
-            ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[t], static_cast<uint32_t>((n - 1) & 1), kWaitNs));
+            ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[t], static_cast<uint32_t>((n - 1) & 1), a.wait_ns));
             tc_fence_after_sync();
           }
           tmem_st_16cols_async(tp + 16 * q2, w);
@@ -629,8 +628,11 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[t]);
       }
-      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[t], static_cast<uint32_t>((n - 1) & 1), kWaitNs) && !*abort_flag);
-      if (!ok && lane == 0) fail(DEV_WAIT_TIMEOUT_EPILOGUE);
+      if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[t], static_cast<uint32_t>((n - 1) & 1), a.wait_ns) && !*abort_flag);
+      if (!ok) {
+        tmem_st_wait();  // of weights that no MMA will take
+        if (lane == 0) fail(DEV_WAIT_TIMEOUT_EPILOGUE);
+      }
       tc_fence_after_sync();
     }
     bool have = ok && nb > 0;
@@ -669,7 +671,19 @@ __global__ void __launch_bounds__(512, 1) paged_attn_tile_kernel(PagedAttnArgs a
     const bool split = a.plan.n_splits > 1;
     const int64_t prow = (static_cast<int64_t>(z) * a.q.n_tok + tok) * a.Hq + hq;
     const float il = l == 0.f ? 0.f : 1.f / l;
-    if (active && !(alt && t == 1)) {
+    if (active && nb > 0 && !have && !(alt && t == 1)) {
+      // a wait ran out: the rows say so, with every range they are joined from
+      if (valid) {
+        if (split) {
+          a.part_ml[prow] = make_float2(0.f, NAN);
+        } else {
+          T* dst = static_cast<T*>(a.out) + tok * a.out_tok + hq * a.out_head;
+#pragma unroll 1
+          for (int d = 0; d < D; ++d) dst[d] = from_f<T>(NAN);
+          if (a.lse) a.lse[static_cast<int64_t>(tok) * a.Hq + hq] = NAN;
+        }
+      }
+    } else if (active && !(alt && t == 1)) {
       // The warp turns its rows through its part of the Q tile (every S is done), 256 bytes of a row at a
       // time, so that 16 lanes write them side by side.
       uint8_t* turn = smem + t * C::kOp + (warp & 3) * (C::kOp / 4);

@@ -177,7 +177,7 @@ def pcd_k_kv_append(k, v, k_cache, v_cache, k_scale, v_scale, q_off, kv_len, tab
     (`table` may be a column slice of a wider one: a length beyond its own columns
     is out of range.)
     `err` (int32, one element) is set nonzero when offsets, lengths or pages
-    were out of range."""
+    were out of range; without it, what was skipped goes unsaid."""
     c, dev, _, kv_heads, dim = _pages(k_cache, v_cache, k_scale, v_scale)
     dtype, shape, n_seq = k.dtype, k.shape, kv_len.numel()
     code = _DTYPE.get(dtype)
@@ -218,7 +218,11 @@ def pcd_k_paged_attention(q, k_cache, v_cache, k_scale, v_scale, q_off, kv_len, 
     kv_len, if the caller knows it (default: what the table holds); scale
     defaults to head_dim ** -0.5.  `out` may be q.  Returns the output, and with return_lse the
     log-sum-exp [tokens, query heads] too.  `scratch` (uint8) replaces the
-    workspace that is otherwise taken from torch's allocator."""
+    workspace that is otherwise taken from torch's allocator.  `err` (int32, one
+    element) is set nonzero when offsets, lengths or pages were out of range (such
+    keys are not seen, rows of bad offsets not written), or when a wait of the
+    kernel's pipelines ran out (those rows are NaN); without it, nothing tells of
+    the former."""
     c, dev, page, kv_heads, dim = _pages(k_cache, v_cache, k_scale, v_scale)
     dtype, shape, n_seq = q.dtype, q.shape, kv_len.numel()
     if (dtype is not torch.float16 and dtype is not torch.bfloat16) or len(shape) != 3 or shape[2] != dim:

@@ -150,7 +150,10 @@ int pcd_answer_line(const void* field, int label, const int32_t* sep, int n_sep,
  * follow the conventions above: device pointers, no allocation, no
  * synchronisation, and they may be captured into CUDA graphs.  What they find
  * wrong in device arrays (offsets, lengths, pages out of range) is skipped
- * and recorded as a nonzero code in `dev_err` (device int, may be NULL).
+ * and recorded as a nonzero code in `dev_err` (device int, may be NULL).  So is
+ * a wait inside pcd_k_paged_attention's pipelines that runs out (2 s, or the
+ * PCD_WAIT_LIMIT_MS of the process's first call); the rows it should have
+ * computed are then NaN, and their log-sum-exp too.
  * pcd_last_error() says why a call was refused. */
 #define PCD_DTYPE_F16 3 /* beside PCD_DTYPE_F32 and PCD_DTYPE_BF16 of pcd.h */
 

@@ -2,6 +2,9 @@
 allows them and programs make them: block tables cut out of wider ones, bad
 offsets and lengths beside good ones, outputs in odd places."""
 import math
+import os
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -294,3 +297,15 @@ def test_rows_that_require_a_gradient(paged):  # noqa: F811
             assert torch.equal(paged.pcd_k_paged_attention(x, *cache, q_off, kv_len, table), want[1])
     with torch.inference_mode():
         assert torch.equal(paged.pcd_k_rope(leaf, freqs), want[0])
+
+
+# --------------------------------------------------------------------- failures
+def test_attention_wait_timeout():
+    """Under a 1 ns wait limit a failed pipeline's rows are NaN and reported,
+    and the others right (in a child process: the limit is the process's)."""
+    import paged_timeout_worker as wk
+    env = {**os.environ, "PCD_WAIT_LIMIT_MS": "0.000001"}
+    r = subprocess.run([sys.executable, wk.__file__], env=env, capture_output=True, text=True, timeout=600)
+    assert r.returncode == 0, r.stdout + r.stderr
+    assert "other calls ok" in r.stdout, r.stdout
+    print(r.stdout)
