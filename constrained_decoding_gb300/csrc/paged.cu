@@ -421,7 +421,8 @@ namespace {
 //   O += w v8,  l += w / sv,   out = O / l
 // so the value's scale rides in the exponent: w <= 2^15 fits fp16 whatever the
 // scales, and no value is rounded before the product.  Weights 2^-33 of the
-// largest are the first that fp16 loses; l keeps them in fp32.
+// largest are the first that fp16 loses; l keeps them in fp32, down to 2^-126,
+// which is enough for value scales 2^100 apart.
 //
 // The channel order inside a dot product is free, so the K fragments are taken
 // as each lane's 16 consecutive bytes (Q's fragments are loaded in the same

@@ -262,10 +262,13 @@ int pcd_k_kv_append_cols(const pcd_kv_pages* cache, const void* k, const void* v
  * scores, to join the result with attention over other keys.  A row that sees
  * nothing gives zeros and -inf.  Scores, softmax sums and the output are
  * accumulated in fp32; codes enter the products exactly and a value's scale
- * joins the softmax weight before its rounding to fp16.  Keys of a page that
- * the table has out of range are not seen; a length beyond the table reads as
- * zero tokens.  `out` may be q's own view; another overlap is refused, as are
- * strides that put two of its rows in one place.
+ * joins the softmax weight before its rounding to fp16 (the value scales that a
+ * row sees may lie 2^100 apart).  A cache that was not written here holds no NaN
+ * code (e4m3 0x7f, 0xff): it would reach rows that do not see its token; a NaN or
+ * infinite scale reaches only rows that do.  Keys of a page that the table has
+ * out of range are not seen; a length beyond the table reads as zero tokens.
+ * `out` may be q's own view; another overlap is refused, as are strides that put
+ * two of its rows in one place.
  * max_kv: the longest kv_len, as far as the host knows it; it sets how many
  * key ranges run side by side, not what is computed.  `scratch`: 16-byte
  * aligned, at least pcd_k_paged_attention_scratch_bytes (the same sizes, the

@@ -309,3 +309,28 @@ def test_attention_wait_timeout():
     assert r.returncode == 0, r.stdout + r.stderr
     assert "other calls ok" in r.stdout, r.stdout
     print(r.stdout)
+
+
+# ----------------------------------------------------------------------- scales
+@pytest.mark.parametrize("dtype,lo,hi", [("f16", -33, 7), ("bf16", -20, 20), ("bf16", -60, 40)])
+@pytest.mark.parametrize("q_len,hint", CUTS)
+def test_attention_value_scales_far_apart(paged, q_len, hint, dtype, lo, hi):  # noqa: F811
+    """Blocks whose value scales lie 2^40 and 2^100 apart, in falling, rising
+    and random order, beside blocks of scale zero and sharp scores.  The bounds
+    are those of every other call: a weight's share of O that fp16 loses is
+    2^-33 of the largest, and fp32 weights of under 2^-126, which the normaliser
+    would miss, lie 2^-134 below the largest times its scale, so 2^-34 below its
+    softmax weight at 2^100."""
+    q, kc, vc, ks, vs, q_off, kv_len, table = attend_case("int8", dtype, 16, 128, 7, 1, [q_len, q_len], [400, 250], 3)
+    ks *= torch.exp2(torch.randint(-4, 4, ks.shape, generator=gen(3), device="cuda").float())
+    pages = table[0, :25].long()
+    for order in ("falls", "rises", "random"):
+        e = torch.linspace(hi, lo, 25, device="cuda").round() if order != "random" else \
+            torch.randint(lo, hi + 1, (25,), generator=gen(2), device="cuda").float()
+        vs[:] = 2.0 ** lo
+        vs[pages, 0] = torch.exp2(e.flip(0) if order == "rises" else e)
+        vs[pages[3]] = 0.0
+        a = (q, kc, vc, ks, vs, q_off, kv_len, table)
+        for causal in (True, False):
+            got, lse = paged.pcd_k_paged_attention(*a, max_kv=hint, causal=causal, return_lse=True)
+            check_attend(got, lse, R.attention(*a, causal, 128 ** -0.5))
