@@ -1160,15 +1160,22 @@ void plan_paged_attention(int n_tok, int n_seq, int G, int Hkv, int64_t max_kv, 
     // CTAs, each 8 to start and end and 1.9 a key block, then the join's launch and
     // the parts written and read (1 KB each).  Against one wave where that fits and
     // else no ranges: 26 prompts of 4 to 90 tokens behind 7 k keys, 24 heads, 225 us
-    // for 241; 22 of 186 tokens, heads of 64, 169 for 176.
+    // for 241; 22 of 186 tokens, heads of 64, 169 for 176.  More than 32 MiB
+    // of parts have to promise a twentieth, and 512 MiB is the most: 8192 tokens of 64
+    // heads at the end of 131072 keys, promised 2.4%, took 26.9 ms in two ranges and
+    // 545 MB against 26.3 in one; 3630 of 24 heads at 9812, 3%, 389 us and 91 MB against
+    // 352; 2048 of 64 at 131072, 13%, 7.07 ms in five against 7.70.  Less is worth small
+    // gains: 26 x 41 tokens of 7 heads at 929 keys, 2.7%, 24.8 us in two against 25.9.
     const int64_t blocks = std::max<int64_t>(1, (max_kv + 127) / 128);
-    double best = 0.0;
+    const double range_bytes = static_cast<double>(n_tok) * G * Hkv * (128 * 4 + 8);
+    double best = 0.0, one = 0.0;
     want = 1;
     for (int64_t n = 1; n <= std::min(blocks, std::max<int64_t>(8, sms / tiles)); ++n) {
       const double waves = static_cast<double>((tiles * n + sms - 1) / sms);
       const double t = waves * (8.0 + 1.9 * static_cast<double>((blocks + n - 1) / n)) +
                        (n > 1 ? 4.0 + n * static_cast<double>(n_tok) * G * Hkv * 2e-4 : 0.0);
-      if (n == 1 || t < best) best = t, want = n;
+      if (n == 1) best = one = t;
+      else if (t < best && (n * range_bytes <= 33554432.0 || (t < 0.95 * one && n * range_bytes <= 536870912.0))) best = t, want = n;
     }
   }
   p->n_splits = static_cast<int>(std::max<int64_t>(want, 1));

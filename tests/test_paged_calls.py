@@ -90,3 +90,22 @@ def test_frequencies_at_the_ends_of_the_scalings(lib, scaling, orig, lo, hi):  #
             assert got == pytest.approx(f / factor, rel=1e-12), i
         else:
             assert f / factor * (1 - 1e-12) <= got <= f * (1 + 1e-12), i
+
+
+# -------------------------------------------------------------------- workspace
+@pytest.mark.parametrize("n_tok,heads,kv_heads,max_kv", [(8192, 64, 8, 131072), (4096, 64, 8, 1 << 20), (4096, 64, 8, 131072), (65536, 128, 8, 1 << 20)])
+def test_long_prompts_need_no_workspace(lib, n_tok, heads, kv_heads, max_kv):  # noqa: F811
+    """Where the query rows alone fill the GPU, ranges of keys would cost
+    hundreds of MB for no time."""
+    assert lib.pcd_k_paged_attention_scratch_bytes(n_tok, 1, heads, kv_heads, 128, max_kv) == 0
+
+
+def test_workspace_is_bounded(lib):  # noqa: F811
+    b = lib.pcd_k_paged_attention_scratch_bytes
+    assert b(1024, 1, 64, 8, 128, 131072) > 0  # few rows: ranges of keys
+    for n_tok in (64, 313, 1000, 1024, 2048, 3000, 5000, 20000):
+        for n_seq in (1, 3, 17):
+            for heads, kv_heads in ((8, 8), (28, 4), (64, 8), (128, 1)):
+                for max_kv in (900, 8192, 131072, 1 << 20, 1 << 31):
+                    if n_tok * heads // kv_heads > 32 * n_seq:
+                        assert b(n_tok, n_seq, heads, kv_heads, 128, max_kv) <= 1 << 29
