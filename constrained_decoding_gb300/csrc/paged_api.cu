@@ -105,10 +105,16 @@ bool rows_overlap(int64_t width, Axis* ax, int k) {
   return false;
 }
 bool rows_overlap(int64_t es, int64_t n, int64_t h, int64_t d, int64_t tok, int64_t head) {
+  if (head >= d && tok >= static_cast<__int128>(h - 1) * head + d) return false;  // as nearly always: heads within a token
   Axis ax[2] = {{tok * es, n}, {head * es, h}};
   return rows_overlap(d * es, ax, 2);
 }
 bool codes_overlap(const pcd::PagesView& c) {
+  // as nearly always: slots within heads or heads within slots, both within pages
+  const int64_t slots = int64_t{1} << c.page_log2, lo = std::min(c.tok_stride, c.head_stride), hi = std::max(c.tok_stride, c.head_stride);
+  const int64_t n_lo = c.tok_stride < c.head_stride ? slots : c.Hkv, n_hi = c.tok_stride < c.head_stride ? c.Hkv : slots;
+  const __int128 inner = static_cast<__int128>(n_lo - 1) * lo + c.dim;
+  if (lo >= c.dim && hi >= inner && c.page_stride >= static_cast<__int128>(n_hi - 1) * hi + inner) return false;
   Axis ax[3] = {{c.page_stride, c.n_pages}, {c.head_stride, c.Hkv}, {c.tok_stride, int64_t{1} << c.page_log2}};
   return rows_overlap(c.dim, ax, 3);
 }
@@ -117,8 +123,11 @@ bool keys_meet_values(const pcd::PagesView& c) {
   const int64_t scales = static_cast<int64_t>(c.n_pages) * c.Hkv;
   if (c.ks < c.vs + scales && c.vs < c.ks + scales) return true;
   Axis ax[3] = {{c.page_stride, c.n_pages}, {c.head_stride, c.Hkv}, {c.tok_stride, int64_t{1} << c.page_log2}};
-  const int k = order_axes(ax, 3);
   const __int128 delta = reinterpret_cast<intptr_t>(c.v) - reinterpret_cast<intptr_t>(c.k);
+  __int128 span = c.dim;
+  for (const Axis& a : ax) span += static_cast<__int128>(a.n - 1) * a.stride;
+  if (delta >= span || -delta >= span) return false;
+  const int k = order_axes(ax, 3);
   return rows_meet(delta, c.dim, ax, k, true);
 }
 
@@ -163,13 +172,15 @@ int view_seqs(const int32_t* q_off, const int32_t* kv_len, const int32_t* table,
 bool views_ok(const void* x, const void* y, int64_t es, int64_t n, int64_t h, int64_t d, int64_t xt, int64_t xh, int64_t yt,
               int64_t yh) {
   const int64_t xa = reinterpret_cast<int64_t>(x), ya = reinterpret_cast<int64_t>(y);
-  if ((xt == yt || n <= 1) && (xh == yh || h <= 1)) {
-    Axis ax[2] = {{yt * es, n}, {yh * es, h}};
-    const int k = order_axes(ax, 2);
-    return x == y || !rows_meet(ya - xa, d * es, ax, k, true);
-  }
+  const bool same = (xt == yt || n <= 1) && (xh == yh || h <= 1);
+  if (x == y && same) return true;
   const int64_t xs = ((n - 1) * xt + (h - 1) * xh + d) * es, ys = ((n - 1) * yt + (h - 1) * yh + d) * es;
   if (xa + xs <= ya || ya + ys <= xa) return true;
+  if (same) {
+    Axis ax[2] = {{yt * es, n}, {yh * es, h}};
+    const int k = order_axes(ax, 2);
+    return !rows_meet(ya - xa, d * es, ax, k, true);
+  }
   if (xt != yt || xt <= 0) return false;
   // rows interleave: side by side within the common token stride
   const int64_t row = xt * es, xr = ((h - 1) * xh + d) * es, yr = ((h - 1) * yh + d) * es;

@@ -71,16 +71,25 @@ def _rope(freqs, dev: int, dim: int):
     return freqs.data_ptr(), rot
 
 
-def _rows(t, dev: int, shape, dtype, what: str):
-    """The strides of a [tokens, heads, dim] tensor of this shape and type on device `dev`."""
+def _too_many():
+    raise ValueError("under 2^31 tokens, heads, sequences and pages a sequence")
+
+
+def _strides(t, dev: int, dim: int, what: str):
+    """The strides of a [tokens, heads, dim] tensor on device `dev`."""
     st = t.stride()
-    if t.get_device() != dev or t.shape != shape or t.dtype is not dtype or (st[2] != 1 and shape[2] != 1):
-        raise ValueError(f"{what}: {list(shape)} of {dtype} on cuda:{dev}, channels contiguous")
+    if t.get_device() != dev or (st[2] != 1 and dim != 1):
+        raise ValueError(f"{what}: on cuda:{dev}, channels contiguous")
     if t.requires_grad and torch.is_grad_enabled():
         raise ValueError(f"{what}: requires a gradient, which this call does not record")
-    if shape[0] > _INT or shape[1] > _INT:
-        raise ValueError(f"{what}: under 2^31 rows and heads")
     return st
+
+
+def _rows(t, dev: int, shape, dtype, what: str):
+    """... that has this shape and type too."""
+    if t.shape != shape or t.dtype is not dtype:
+        raise ValueError(f"{what}: {list(shape)} of {dtype}")
+    return _strides(t, dev, shape[2], what)
 
 
 def _launch(dev: int, where: str, fn, *args) -> None:
@@ -123,9 +132,11 @@ def pcd_k_rope(x, freqs, pos=None, *, base: int = 0, interleaved: bool = False, 
     if code is None or dev < 0 or len(shape) != 3:
         raise ValueError("x: a float32, float16 or bfloat16 CUDA tensor [tokens, heads, dim]")
     n, heads, dim = shape
-    xs = _rows(x, dev, shape, dtype, "x")
+    if n > _INT or heads > _INT:
+        _too_many()
+    xs = _strides(x, dev, dim, "x")
     f, rot = _rope(freqs, dev, dim)
-    if not -0x80000000 <= base <= 0x7fffffff:
+    if base and not -0x80000000 <= base <= _INT:
         raise ValueError("base: a 32-bit integer")
     if out is None:
         out = torch.empty(shape, dtype=dtype, device=x.device)
@@ -159,13 +170,17 @@ def _pages(k_cache, v_cache, k_scale, v_scale):
 
 def _table(table, n_seq: int, dev: int):
     """(pointer, row stride, width) of a block table."""
-    shape, st = table.shape, table.stride()
-    if (table.dtype is not _int32 or table.get_device() != dev or len(shape) != 2 or shape[0] != n_seq or
-            (st[1] != 1 and shape[1] > 1) or (st[0] < shape[1] and n_seq > 1)):
-        raise ValueError(f"table: int32 [{n_seq}, pages] on cuda:{dev}, rows contiguous")
-    if n_seq > _INT or shape[1] > _INT or (st[0] > _INT and n_seq > 1):
-        raise ValueError("table: under 2^31 sequences and pages")
-    return table.data_ptr(), st[0] if n_seq > 1 else shape[1], shape[1]
+    shape = table.shape
+    if table.dtype is _int32 and table.get_device() == dev and len(shape) == 2:
+        n, width = shape
+        stride, step = table.stride()
+        if n_seq < 2:
+            stride = width
+        if n == n_seq and (step == 1 or width < 2) and stride >= width:
+            if n + stride > _INT:
+                _too_many()
+            return table.data_ptr(), stride, width
+    raise ValueError(f"table: int32 [{n_seq}, pages] on cuda:{dev}, rows contiguous")
 
 
 def pcd_k_kv_append(k, v, k_cache, v_cache, k_scale, v_scale, q_off, kv_len, table, *, freqs=None,
@@ -184,7 +199,9 @@ def pcd_k_kv_append(k, v, k_cache, v_cache, k_scale, v_scale, q_off, kv_len, tab
     if code is None or len(shape) != 3 or shape[1] != kv_heads or shape[2] != dim:
         raise ValueError("k: float32, float16 or bfloat16 [tokens, KV heads, head dim]")
     n = shape[0]
-    ks, vs = _rows(k, dev, shape, dtype, "k"), _rows(v, dev, shape, dtype, "v")
+    if n > _INT:
+        _too_many()
+    ks, vs = _strides(k, dev, dim, "k"), _rows(v, dev, shape, dtype, "v")
     t, t_stride, width = _table(table, n_seq, dev)
     f, rot = _rope(freqs, dev, dim)
     _launch(dev, "pcd_k_kv_append", _lib.pcd_k_kv_append_cols, c, k.data_ptr(), v.data_ptr(), code, ks[0], ks[1],
@@ -195,7 +212,7 @@ def pcd_k_kv_append(k, v, k_cache, v_cache, k_scale, v_scale, q_off, kv_len, tab
 def pcd_k_paged_attention_scratch_bytes(n_tok: int, n_seq: int, n_q_heads: int, n_kv_heads: int, head_dim: int,
                                         max_kv: int) -> int:
     if max(n_tok, n_seq, n_q_heads, n_kv_heads, head_dim) > _INT:
-        raise ValueError("sizes under 2^31")
+        _too_many()
     return int(_lib.pcd_k_paged_attention_scratch_bytes(n_tok, n_seq, n_q_heads, n_kv_heads, head_dim, max_kv))
 
 
@@ -228,7 +245,9 @@ def pcd_k_paged_attention(q, k_cache, v_cache, k_scale, v_scale, q_off, kv_len, 
     if (dtype is not torch.float16 and dtype is not torch.bfloat16) or len(shape) != 3 or shape[2] != dim:
         raise ValueError("q: float16 or bfloat16 [tokens, heads, head dim]")
     n, heads, _ = shape
-    qs = _rows(q, dev, shape, dtype, "q")
+    if n > _INT or heads > _INT:
+        _too_many()
+    qs = _strides(q, dev, dim, "q")
     t, t_stride, width = _table(table, n_seq, dev)
     if out is None:
         out = torch.empty(shape, dtype=dtype, device=q.device)
