@@ -23,7 +23,7 @@ namespace {
 // layout) of every hgs-th head of one token, so an angle's sine and cosine are
 // computed once for all of them, and takes two heads' loads at a time (four cost
 // registers and 4 us of 25 at 8192 tokens x 32 heads).  That call, fp16 heads of
-// 128: 24.7 us, 5.4 TB/s; 64 tokens of 14 heads 2.1 us.
+// 128: 26.5 us, 5.1 TB/s; 64 tokens of 14 heads 2.5 us.
 // VEC: the widest access that pointers, strides and the pair layout allow.
 template <class T, int N>
 struct alignas(sizeof(T) * N) Chunk {
@@ -141,8 +141,10 @@ namespace {
 // comes out the same on every run.
 //   amax over the new rows -> scale (grown, never shrunk, while older tokens
 //   stay in the page) -> older codes rescaled if it grew -> new codes.
-// Bound by that chain: 14.4 k tokens of four fp16 heads of 128 take 15 to 17 us
-// (2.7 TB/s of rows read and codes written), one token each of 64 sequences 5 us.
+// One token each of 64 sequences takes 5 us, that chain; 14.4 k tokens of four fp16
+// heads of 128 17 us (2.6 TB/s of rows read and codes written), 13 with the rows in
+// L2, bound by what is in flight: 120 registers let two CTAs on an SM, each with
+// one head's rows (16 KB) ahead, and the last of its CTAs start in a second wave.
 // The block of a CTA: its new rows and where they go.
 struct AppendBlock {
   int held, rows, row0, pos0;  // older tokens in the page; new rows, the first one's index and position
@@ -437,9 +439,10 @@ namespace {
 // contexts of up to 600: 43 against 53).
 //
 // Bound by the bytes of the pages: 64 contexts of 4 to 12 k keys 89 us, 5.8
-// TB/s; three of 131 k int8 keys 76 us, 5.3 TB/s.  Each warp has three blocks of
-// its ring in flight, 144 KB an SM; a fourth stage or CTA took 115 to 120 us for
-// the former, two stages 92.  One context of 901 keys 8 us, a chain of trips.
+// TB/s; three of 131 k int8 keys 73 us, 5.5 TB/s.  Each warp has two blocks in
+// flight while it works on the third of its ring, 96 KB an SM of the rings' 144;
+// three in flight (a fourth stage) or a fourth CTA took 115 to 120 us for the
+// former, one in flight 92.  One context of 901 keys 8 us, a chain of trips.
 //
 // How the work is cut: small calls give every item (a tile of one KV head) to a
 // thread-block cluster of up to 8 CTAs that divide its keys and join through

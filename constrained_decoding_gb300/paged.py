@@ -190,7 +190,7 @@ def pcd_k_kv_append(k, v, k_cache, v_cache, k_scale, v_scale, q_off, kv_len, tab
     Rows q_off[s] .. q_off[s + 1) become the last tokens of sequence s, which has
     kv_len[s] with them; token j of it lies in page table[s, j // page size].
     (`table` may be a column slice of a wider one: a length beyond its own columns
-    is out of range.)
+    is out of range.)  A page that the call writes to stands once in the table.
     `err` (int32, one element) is set nonzero when offsets, lengths or pages
     were out of range; without it, what was skipped goes unsaid."""
     c, dev, _, kv_heads, dim = _pages(k_cache, v_cache, k_scale, v_scale)

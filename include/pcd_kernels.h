@@ -1,6 +1,7 @@
-/* Kernel-level entry points of the PCD library, for testing one device step
- * in isolation against the CPU oracle.  Every pointer is a DEVICE pointer the
- * caller owns; nothing is allocated or freed here.  Each call is enqueued on
+/* Kernel-level entry points of the PCD library: single device steps, for
+ * testing them in isolation against the CPU oracle, and the operators of a
+ * serving layer (rotary positions, an 8-bit paged cache, attention over it).
+ * Every pointer is a DEVICE pointer the caller owns; nothing is allocated or freed here.  Each call is enqueued on
  * `stream` (a cudaStream_t, NULL = legacy default stream) and returns without
  * synchronising.  Return value: 0 on success, a negative PCD_ERR_* code
  * (pcd.h) for invalid arguments, or PCD_ERR_CUDA when the launch fails.
@@ -238,7 +239,7 @@ typedef struct {
  * two, exact while they stay normal; int8: rounded once more).  Codes round to
  * nearest even.  A NaN or infinity in a block's rows makes its scale so, and
  * all that is read from that block NaN.  A page that one call appends to
- * belongs to one sequence.  Nothing but the new tokens' pages is written.
+ * belongs to one sequence and stands once in its row of the table.  Nothing but the new tokens' pages is written.
  * Strides that put two rows of the cache in one place are refused, and keys and
  * values in one place. */
 int pcd_k_kv_append(const pcd_kv_pages* cache, const void* k, const void* v, int dtype, int64_t k_tok, int64_t k_head,
